@@ -367,7 +367,7 @@ def _plain_tables(s):
     need = torch.where(fits, (ln + grow + P - 1) // P - held, 0)
     inc, rinc = need.cumsum(0), grow.cumsum(0)
     ok = (nn >= 0) & fits & ((need == 0) | (inc <= count)) & (rinc <= T)
-    used = torch.where(ok, inc, 0).max()
+    used = torch.where(ok & (need > 0), inc, 0).max()
     seq_len = torch.where(nn < 0, 0, torch.where(ok, ln + grow, ln))
     t = torch.arange(T, device="cuda")
     i = torch.searchsorted(rinc, t, right=True)
