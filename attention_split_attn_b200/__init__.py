@@ -15,7 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -24,6 +24,7 @@ LIB_PATH = os.path.join(_HERE, "libattn_b200.so")
 
 ATTN_F32, ATTN_F16, ATTN_BF16, ATTN_FP8_E4M3, ATTN_I8 = 0, 1, 2, 3, 4
 OP_DECODE, OP_SELECTED, OP_PREFILL, OP_SELECTED_MASKED = 0, 1, 2, 3
+OP_DECODE_PAGED, OP_DECODE_SHARED = 4, 5
 STATUS = {0: "ATTN_OK", -1: "ATTN_ERR_INVALID_ARG", -2: "ATTN_ERR_UNSUPPORTED",
           -3: "ATTN_ERR_WORKSPACE", -4: "ATTN_ERR_CUDA", -5: "ATTN_ERR_DEVICE_TIMEOUT"}
 
@@ -35,6 +36,8 @@ EXPORTS = ("attn_workspace_size", "attn_supports", "attn_decode", "attn_selected
            "attn_prefill", "attn_decode_timed", "attn_selected_timed", "attn_prefill_timed",
            "attn_decode_noalloc", "attn_tree_mask", "attn_selected_masked", "attn_selected_masked_timed",
            "attn_decode_append", "attn_decode_cluster",
+           "attn_page_tables", "attn_append_paged", "attn_paged_supports", "attn_paged_workspace_size",
+           "attn_decode_paged", "attn_decode_shared",
            "attn_check_device_status",
            "attn_strerror", "attn_last_error", "attn_abi_version")
 
@@ -69,6 +72,57 @@ class AttnSelectedArgs(ctypes.Structure):
         ("base", AttnArgs),
         ("sel", ctypes.c_void_p), ("sel_stride_row", ctypes.c_int64), ("n_sel", ctypes.c_int32),
         ("sel_sorted_out", ctypes.c_void_p), ("sel_count_out", ctypes.c_void_p),
+    ]
+
+
+class AttnPageArgs(ctypes.Structure):
+    """Mirror of attn_page_args (include/attn.h)."""
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+        ("table_width", ctypes.c_int32), ("n_rows", ctypes.c_int32),
+        ("seq_len", ctypes.c_void_p), ("new_len", ctypes.c_void_p), ("n_keep", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("free_ring", ctypes.c_void_p), ("free_state", ctypes.c_void_p), ("free_state_out", ctypes.c_void_p),
+        ("slot", ctypes.c_void_p), ("row_seq", ctypes.c_void_p), ("row_end", ctypes.c_void_p),
+        ("seq_row", ctypes.c_void_p), ("seq_len_out", ctypes.c_void_p),
+        ("reserved", ctypes.c_int32 * 4),
+    ]
+
+
+class AttnAppendArgs(ctypes.Structure):
+    """Mirror of attn_append_args (include/attn.h)."""
+    _fields_ = [
+        ("n_rows", ctypes.c_int32), ("n_head_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p), ("new_type", ctypes.c_int32),
+        ("new_stride_row", ctypes.c_int64), ("new_stride_head", ctypes.c_int64),
+        ("slot", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("kv_type", ctypes.c_int32),
+        ("kv_stride_page", ctypes.c_int64), ("kv_stride_cell", ctypes.c_int64), ("kv_stride_head", ctypes.c_int64),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("scale_stride_cell", ctypes.c_int64),
+        ("reserved", ctypes.c_int32 * 4),
+    ]
+
+
+class AttnPagedArgs(ctypes.Structure):
+    """Mirror of attn_paged_args (include/attn.h)."""
+    _fields_ = [
+        ("n_rows", ctypes.c_int32), ("n_head_q", ctypes.c_int32), ("n_head_kv", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("q", ctypes.c_void_p), ("q_type", ctypes.c_int32),
+        ("q_stride_row", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("kv_type", ctypes.c_int32),
+        ("kv_stride_page", ctypes.c_int64), ("kv_stride_cell", ctypes.c_int64), ("kv_stride_head", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("out_type", ctypes.c_int32),
+        ("o_stride_row", ctypes.c_int64), ("o_stride_head", ctypes.c_int64),
+        ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("n_tables", ctypes.c_int32), ("table_width", ctypes.c_int32),
+        ("row_table", ctypes.c_void_p), ("row_begin", ctypes.c_void_p), ("row_end", ctypes.c_void_p),
+        ("n_groups", ctypes.c_int32), ("group_begin", ctypes.c_void_p), ("group_len", ctypes.c_void_p),
+        ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+        ("alibi_slopes", ctypes.c_void_p), ("sinks", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("scale_stride_cell", ctypes.c_int64),
+        ("reserved", ctypes.c_int32 * 4),
     ]
 
 
@@ -128,6 +182,18 @@ def load_library():
             lib.attn_tree_mask.restype = ctypes.c_int32
             lib.attn_tree_mask.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                            ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]
+            lib.attn_page_tables.restype = ctypes.c_int32
+            lib.attn_page_tables.argtypes = [ctypes.POINTER(AttnPageArgs), ctypes.c_void_p]
+            lib.attn_append_paged.restype = ctypes.c_int32
+            lib.attn_append_paged.argtypes = [ctypes.POINTER(AttnAppendArgs), ctypes.c_void_p]
+            lib.attn_paged_supports.restype = ctypes.c_int32
+            lib.attn_paged_supports.argtypes = [ctypes.POINTER(AttnPagedArgs), ctypes.c_int32]
+            lib.attn_paged_workspace_size.restype = ctypes.c_size_t
+            lib.attn_paged_workspace_size.argtypes = [ctypes.POINTER(AttnPagedArgs), ctypes.c_int32]
+            for name in ("attn_decode_paged", "attn_decode_shared"):
+                fn = getattr(lib, name)
+                fn.restype = ctypes.c_int32
+                fn.argtypes = [ctypes.POINTER(AttnPagedArgs), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
             lib.attn_check_device_status.restype = ctypes.c_int32
             lib.attn_check_device_status.argtypes = [ctypes.c_void_p]
             lib.attn_strerror.restype = ctypes.c_char_p
@@ -146,7 +212,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 def _check_i32(name, t, n):
     if t is None:
         return
-    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or t.stride(0) != 1 or t.numel() < n:
+    if (t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1)
+            or t.numel() < n):
         raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of at least {n} entries")
 
 
@@ -427,6 +494,220 @@ def tree_mask(parent: torch.Tensor, prefix_cells: int, n_cells: int, mask: Optio
     _raise_if(lib.attn_tree_mask(parent.data_ptr(), R, int(prefix_cells), int(n_cells), mask.data_ptr(),
                                  mask.stride(0), _stream_handle(stream)), "attn_tree_mask")
     return mask
+
+
+# ----------------------------------------------------------------------------
+# Paged caches (see include/attn.h)
+# ----------------------------------------------------------------------------
+
+class PageTables(NamedTuple):
+    """What attn_page_tables writes, beside the block tables and the ring."""
+    slot: torch.Tensor         # [n_rows] pool slot of each row, -1 for padding
+    row_seq: torch.Tensor      # [n_rows] the row's sequence, -1 behind the last
+    row_end: torch.Tensor      # [n_rows] cells the row may see
+    seq_row: torch.Tensor      # [n_seqs + 1] first row of each sequence
+    seq_len: torch.Tensor      # [n_seqs] lengths after the step
+    free_state: torch.Tensor   # [2] ring state after the step
+
+
+def _on_device(a, *tensors):
+    """All tensors on one CUDA device, kept with the argument block for the calls."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) > 1 or any(d.type != "cuda" for d in devs):
+        raise ValueError(f"tensors must be on one CUDA device, got {sorted(map(str, devs))}")
+    a.device = next(iter(devs)).index
+    return a
+
+
+def _stream_on(a, stream) -> int:
+    """The stream handle of a call; its device must be the current one (the kernels launch there)."""
+    cur = torch.cuda.current_device()
+    if a.device != cur:
+        raise ValueError(f"tensors are on cuda:{a.device}, the current device is cuda:{cur}")
+    return _stream_handle(stream)
+
+
+def _check_pool(k, v):
+    if k.dim() != 4 or v.dim() != 4:
+        raise ValueError("k, v must be [pages, cells per page, heads, dim]")
+    if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+        raise ValueError("k and v must share shape, strides and dtype")
+    if k.dtype not in _DTYPE:
+        raise ValueError(f"unsupported cache dtype {k.dtype}")
+    if k.stride(3) != 1:
+        raise ValueError("k, v: the head dimension must be contiguous")
+
+
+def _set_pool(a, k, v, k_scale, v_scale):
+    n_pages, P, Hkv, D = k.shape
+    a.n_head_kv, a.head_dim, a.n_pages, a.page_size = Hkv, D, n_pages, P
+    a.k, a.v, a.kv_type = k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype]
+    a.kv_stride_page, a.kv_stride_cell, a.kv_stride_head = k.stride(0), k.stride(1), k.stride(2)
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale must both be given or both be None")
+    if k_scale is not None:
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.dtype != torch.float32 or tuple(t.shape) != (n_pages * P, Hkv) or t.stride(1) != 1:
+                raise ValueError(f"{name} must be float32 [pages * cells per page, n_head_kv] with contiguous heads")
+        if k_scale.stride(0) != v_scale.stride(0):
+            raise ValueError("k_scale and v_scale must share their cell stride")
+        a.k_scale, a.v_scale, a.scale_stride_cell = k_scale.data_ptr(), v_scale.data_ptr(), k_scale.stride(0)
+
+
+def make_page_args(seq_len, new_len, page_table, free_ring, free_state, *, page_size, n_rows, n_keep=None,
+                   outputs: Optional[PageTables] = None):
+    """Fill an AttnPageArgs: seq_len, new_len [n_seqs], page_table [n_seqs,
+    width] and free_ring [n_pages] are int32 CUDA tensors (the last two are
+    updated by the call), free_state int32 [2].  outputs (a PageTables of int32
+    tensors) is allocated when not given and kept as `.outputs`."""
+    n = seq_len.numel()
+    for name, t, m in (("seq_len", seq_len, n), ("new_len", new_len, n), ("free_ring", free_ring, 0),
+                       ("free_state", free_state, 2), ("n_keep", n_keep, n)):
+        _check_i32(name, t, m)
+    if (page_table.dtype != torch.int32 or not page_table.is_cuda or page_table.dim() != 2
+            or page_table.shape[0] < n or (page_table.numel() > 1 and page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise ValueError("page_table must be an int32 CUDA tensor [n_seqs, width] with contiguous entries")
+    if outputs is None:
+        new = lambda m: torch.empty(m, dtype=torch.int32, device=seq_len.device)
+        outputs = PageTables(new(n_rows), new(n_rows), new(n_rows), new(n + 1), new(n), new(2))
+    for name, t, m in zip(PageTables._fields, outputs, (n_rows, n_rows, n_rows, n + 1, n, 2)):
+        _check_i32(name, t, m)
+    a = AttnPageArgs()
+    a.n_seqs, a.page_size, a.n_pages = n, int(page_size), free_ring.numel()
+    a.table_width, a.n_rows = page_table.shape[1], int(n_rows)
+    a.seq_len, a.new_len, a.n_keep = seq_len.data_ptr(), new_len.data_ptr(), _ptr(n_keep)
+    a.page_table, a.table_stride = page_table.data_ptr(), page_table.stride(0)
+    a.free_ring, a.free_state = free_ring.data_ptr(), free_state.data_ptr()
+    a.slot, a.row_seq, a.row_end, a.seq_row, a.seq_len_out, a.free_state_out = (_ptr(t) for t in outputs)
+    a.outputs = outputs
+    return _on_device(a, seq_len, new_len, page_table, free_ring, free_state, n_keep, *outputs)
+
+
+def attn_page_tables_args(args: AttnPageArgs, stream=None) -> PageTables:
+    """attn_page_tables on a prepared AttnPageArgs; returns its outputs."""
+    st = load_library().attn_page_tables(ctypes.byref(args), _stream_on(args, stream))
+    _raise_if(st, "attn_page_tables")
+    return args.outputs
+
+
+def page_tables(seq_len, new_len, page_table, free_ring, free_state, *, stream=None, **kw) -> PageTables:
+    """Grow and release the sequences' block tables for one step and write its
+    slot map and row ranges (see include/attn.h)."""
+    return attn_page_tables_args(make_page_args(seq_len, new_len, page_table, free_ring, free_state, **kw), stream)
+
+
+def make_append_args(k_new, v_new, slot, k, v, *, k_scale=None, v_scale=None):
+    """Fill an AttnAppendArgs: k_new, v_new [rows, n_head_kv, dim], slot int32
+    [rows], k, v the cache [pages, cells per page, n_head_kv, dim] (any order in
+    memory with the dim contiguous), scales [pages * cells per page, n_head_kv]."""
+    _check_pool(k, v)
+    if k_new.dim() != 3 or k_new.shape != v_new.shape or k_new.stride() != v_new.stride() or k_new.dtype != v_new.dtype:
+        raise ValueError("k_new and v_new must be [rows, n_head_kv, dim] and share shape, strides and dtype")
+    if k_new.stride(2) != 1 or k_new.dtype not in _DTYPE or tuple(k_new.shape[1:]) != tuple(k.shape[2:]):
+        raise ValueError("k_new, v_new: heads and dim as the cache's, the head dimension contiguous")
+    _check_i32("slot", slot, k_new.shape[0])
+    a = AttnAppendArgs()
+    a.n_rows = k_new.shape[0]
+    a.k_new, a.v_new, a.new_type = k_new.data_ptr(), v_new.data_ptr(), _DTYPE[k_new.dtype]
+    a.new_stride_row, a.new_stride_head = k_new.stride(0), k_new.stride(1)
+    a.slot = slot.data_ptr()
+    _set_pool(a, k, v, k_scale, v_scale)
+    return _on_device(a, k_new, v_new, slot, k, v, k_scale, v_scale)
+
+
+def attn_append_paged_args(args: AttnAppendArgs, stream=None):
+    """attn_append_paged on a prepared AttnAppendArgs."""
+    _raise_if(load_library().attn_append_paged(ctypes.byref(args), _stream_on(args, stream)), "attn_append_paged")
+
+
+def append_paged(k_new, v_new, slot, k, v, *, stream=None, **kw):
+    """Write new K/V rows through a slot map into a paged cache (see include/attn.h)."""
+    attn_append_paged_args(make_append_args(k_new, v_new, slot, k, v, **kw), stream)
+
+
+def make_paged_args(q, k, v, out, page_table, row_end, *, scale, softcap=0.0, row_begin=None, row_table=None,
+                    group_begin=None, group_len=None, alibi_slopes=None, sinks=None, k_scale=None, v_scale=None):
+    """Fill an AttnPagedArgs: q, out [rows, n_head_q, dim], k, v [pages, cells
+    per page, n_head_kv, dim], page_table int32 [tables, width], row_end (and
+    row_begin, row_table) int32 [rows]; group_begin int32 [groups + 1] and
+    group_len int32 [groups] for decode_shared."""
+    _check_pool(k, v)
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError("q, out must be [rows, heads, dim]")
+    R, Hq, D = q.shape
+    if k.shape[3] != D:
+        raise ValueError("q and the cache must share the head dimension")
+    for name, t in (("q", q), ("out", out)):
+        if t.stride(2) != 1 or t.dtype not in _DTYPE:
+            raise ValueError(f"{name}: a supported dtype with the head dimension contiguous")
+    if (page_table.dtype != torch.int32 or not page_table.is_cuda or page_table.dim() != 2
+            or (page_table.numel() > 1 and page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise ValueError("page_table must be an int32 CUDA tensor [tables, width] with contiguous entries")
+    if (group_begin is None) != (group_len is None):
+        raise ValueError("group_begin and group_len must both be given or both be None")
+    n_groups = 0 if group_len is None else group_len.numel()
+    for name, t, n in (("row_end", row_end, R), ("row_begin", row_begin, R), ("row_table", row_table, R),
+                       ("group_len", group_len, n_groups), ("group_begin", group_begin, n_groups + 1)):
+        _check_i32(name, t, n)
+    for name, t in (("alibi_slopes", alibi_slopes), ("sinks", sinks)):
+        if t is not None and (t.dtype != torch.float32 or t.numel() < Hq or t.stride(0) != 1):
+            raise ValueError(f"{name} must be a contiguous float32 tensor of n_head_q entries")
+    a = AttnPagedArgs()
+    a.n_rows, a.n_head_q = R, Hq
+    a.q, a.q_type, a.q_stride_row, a.q_stride_head = q.data_ptr(), _DTYPE[q.dtype], q.stride(0), q.stride(1)
+    a.out, a.out_type, a.o_stride_row, a.o_stride_head = out.data_ptr(), _DTYPE[out.dtype], out.stride(0), out.stride(1)
+    _set_pool(a, k, v, k_scale, v_scale)
+    a.page_table, a.table_stride = page_table.data_ptr(), page_table.stride(0)
+    a.n_tables, a.table_width = page_table.shape
+    a.row_table, a.row_begin, a.row_end = _ptr(row_table), _ptr(row_begin), row_end.data_ptr()
+    a.n_groups, a.group_begin, a.group_len = n_groups, _ptr(group_begin), _ptr(group_len)
+    a.scale, a.softcap = float(scale), float(softcap)
+    a.alibi_slopes, a.sinks = _ptr(alibi_slopes), _ptr(sinks)
+    return _on_device(a, q, k, v, out, page_table, row_end, row_begin, row_table, group_begin, group_len,
+                      alibi_slopes, sinks, k_scale, v_scale)
+
+
+def paged_supports(args: AttnPagedArgs, op: int) -> int:
+    return int(load_library().attn_paged_supports(ctypes.byref(args), op))
+
+
+def paged_workspace_size(args: AttnPagedArgs, op: int) -> int:
+    lib = load_library()
+    _raise_if(lib.attn_paged_supports(ctypes.byref(args), op), "attn_paged_supports")
+    return int(lib.attn_paged_workspace_size(ctypes.byref(args), op))
+
+
+def _paged_call(fn, where, args, op, ws, stream):
+    handle = _stream_on(args, stream)
+    if ws is None:
+        ws = _workspace(paged_workspace_size(args, op), torch.device("cuda", args.device), None)
+        if ws is not None and stream is not None:
+            ws.record_stream(stream)   # allocated on the current stream, used on this one
+    st = fn(ctypes.byref(args), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel() * ws.element_size(), handle)
+    _raise_if(st, where)
+    return ws
+
+
+def attn_decode_paged_args(args: AttnPagedArgs, ws: Optional[torch.Tensor] = None, stream=None):
+    """attn_decode_paged on a prepared AttnPagedArgs (workspace allocated if not given)."""
+    return _paged_call(load_library().attn_decode_paged, "attn_decode_paged", args, OP_DECODE_PAGED, ws, stream)
+
+
+def attn_decode_shared_args(args: AttnPagedArgs, ws: Optional[torch.Tensor] = None, stream=None):
+    """attn_decode_shared on a prepared AttnPagedArgs (workspace allocated if not given)."""
+    return _paged_call(load_library().attn_decode_shared, "attn_decode_shared", args, OP_DECODE_SHARED, ws, stream)
+
+
+def decode_paged(q, k, v, out, page_table, row_end, *, ws=None, stream=None, **kw):
+    """Decode attention over a paged cache into `out` (see include/attn.h)."""
+    return attn_decode_paged_args(make_paged_args(q, k, v, out, page_table, row_end, **kw), ws=ws, stream=stream)
+
+
+def decode_shared(q, k, v, out, page_table, row_end, *, ws=None, stream=None, **kw):
+    """Decode attention over a paged cache for groups of rows that share their
+    first cells, which are read once per group (see include/attn.h)."""
+    return attn_decode_shared_args(make_paged_args(q, k, v, out, page_table, row_end, **kw), ws=ws, stream=stream)
 
 
 def check_device_status(stream=None):

@@ -560,6 +560,32 @@ int32_t check_device() {
   DeviceInfo* di = nullptr;
   return device_info(&di);
 }
+int32_t device_facts(int* sms, int** status) {
+  DeviceInfo* di = nullptr;
+  const int32_t st = device_info(&di);
+  if (st != ATTN_OK) return st;
+  *sms = di->sms;
+  *status = di->status;
+  return ATTN_OK;
+}
+int32_t encode_map(CUtensorMap* map, const void* base, int32_t type, int rank, const int64_t* dims,
+                   const int64_t* strides_bytes, const int32_t* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], one[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    b[i] = (cuuint32_t)box[i];
+    one[i] = 1u;
+    if (i + 1 < rank) st[i] = (cuuint64_t)strides_bytes[i];
+  }
+  const CUresult r = enc(map, tma_dtype(type), (cuuint32_t)rank, const_cast<void*>(base), d, st, b, one,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return ATTN_OK;
+}
 }  // namespace attn
 
 using namespace attn;

@@ -156,10 +156,13 @@ struct WarpTileState {
 
   // (one-byte caches load per-cell scales ahead; 16-bit caches have none)
   __device__ __forceinline__ void prefetch(const DecodePlan&, int, int, int) {}
+  __device__ __forceinline__ void prefetch_slot(const DecodePlan&, int, int, int) {}
   __device__ __forceinline__ void take_prefetched() {}
 
   // Fold the loaded tile: cells tile0 .. tile0+15 of the row; only cells
-  // < rc.s_end that pass the row filter count.
+  // < rc.s_end that pass the row filter count (LO: and >= rc.s_begin, for
+  // tiles that start at a multiple of 16 cells instead of at the range).
+  template <bool LO = false>
   __device__ __forceinline__ void compute(const DecodePlan& p, const RowCtx& rc, int r, int tile0,
                                           bool has_filter, int lane, unsigned char* stage) {
     using Op = MmaType<KT>;
@@ -179,7 +182,7 @@ struct WarpTileState {
 #pragma unroll
     for (int kr = 0; kr < 2; ++kr) {
       const int c = tile0 + grp + 8 * kr;
-      bool vk = c < rc.s_end;
+      bool vk = c < rc.s_end && (!LO || c >= rc.s_begin);
       float mval = 0.f;
       float negdist = 0.f;
       if (has_filter || alibi) {

@@ -108,6 +108,16 @@ struct WarpTileState8 {
       nxt_vs[kr] = c < p.N ? __ldg(p.v_scale + si) : 0.f;
     }
   }
+  // The same for a tile of a paged cache, whose 16 cells are the slots slot0
+  // .. slot0 + 15 of the pool (slot0 < 0: no such page, scales of 0).
+  __device__ __forceinline__ void prefetch_slot(const DecodePlan& p, int g, int slot0, int lane) {
+#pragma unroll
+    for (int kr = 0; kr < 2; ++kr) {
+      const int64_t si = ((int64_t)slot0 + (lane >> 2) + 8 * kr) * p.scale_sc + g;
+      nxt_ks[kr] = slot0 >= 0 ? __ldg(p.k_scale + si) : 0.f;
+      nxt_vs[kr] = slot0 >= 0 ? __ldg(p.v_scale + si) : 0.f;
+    }
+  }
   __device__ __forceinline__ void take_prefetched() {
     cur_ks[0] = nxt_ks[0]; cur_ks[1] = nxt_ks[1];
     cur_vs[0] = nxt_vs[0]; cur_vs[1] = nxt_vs[1];
@@ -251,7 +261,8 @@ struct WarpTileState8 {
   }
 
   // Fold the loaded tile: cells tile0 .. tile0+15 of the row; only cells
-  // < rc.s_end that pass the row filter count.
+  // < rc.s_end that pass the row filter count (LO: and >= rc.s_begin).
+  template <bool LO = false>
   __device__ __forceinline__ void compute(const DecodePlan& p, const RowCtx& rc, int r, int tile0,
                                           bool has_filter, int lane, unsigned char* /*stage*/) {
     const int grp = lane >> 2, tig = lane & 3;
@@ -271,7 +282,7 @@ struct WarpTileState8 {
 #pragma unroll
     for (int kr = 0; kr < 2; ++kr) {
       const int c = tile0 + grp + 8 * kr;
-      bool vk = c < rc.s_end;
+      bool vk = c < rc.s_end && (!LO || c >= rc.s_begin);
       float mval = 0.f, negdist = 0.f;
       if (has_filter || alibi) {
         int64_t cpos = (int64_t)c - rc.pos_base;

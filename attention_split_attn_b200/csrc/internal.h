@@ -249,6 +249,43 @@ cudaError_t launch_tree_mask(const int32_t* parent, int32_t n_rows, int32_t pref
                              float* mask, int64_t mask_sr, int* status, cudaStream_t stream);
 int max_tree_rows();
 
+// ---- paged caches ---------------------------------------------------------------
+// A pool of n_pages pages of P cells (P a multiple of 16) and block tables
+// that name each sequence's pages in order: cell c of table i is cell c % P of
+// page table[i][c / P], slot page * P + c % P of the pool.
+struct PagedPlan {
+  DecodePlan d;            // heads, Q, out, logits, scales by slot, partial records, W, row_tiles, status
+  int32_t P, n_pages;
+  const int32_t* table;    // [n_tables][width], rows table_sr apart
+  int64_t table_sr;
+  int32_t n_tables, width;
+  const int32_t* row_table;   // [R] or NULL (row r reads table r)
+  const int32_t* own_lo;      // [R] or NULL: the first cell of row r's own part (shared prefixes)
+};
+
+// Paged decode on the balanced persistent scheme of decode_stream.cu.
+int paged_stream_warps(int kv_type, int D, int G, int sms);
+cudaError_t launch_paged_stream(const PagedPlan& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                cudaStream_t stream);
+
+// Block tables and slot maps from sequence lengths (fields as in attn_page_args).
+struct PageTablesPlan {
+  attn_page_args a;
+  int* status;
+};
+cudaError_t launch_page_tables(const PageTablesPlan& p, int sms, cudaStream_t stream);
+int max_page_seqs();
+
+// New K/V rows written through a slot map (fields as in attn_append_args).
+cudaError_t launch_append_paged(const attn_append_args& a, int sms, cudaStream_t stream);
+
+// Facts of the current device (ATTN_OK, or why it cannot be used).
+int32_t device_facts(int* sms, int** status);
+// A 128-byte-swizzled tile map of `rank` dimensions (strides in bytes, of
+// dimensions 1 .. rank - 1).
+int32_t encode_map(CUtensorMap* map, const void* base, int32_t type, int rank, const int64_t* dims,
+                   const int64_t* strides_bytes, const int32_t* box);
+
 // Set the message attn_last_error() returns on this thread.
 void set_last_error(const char* msg);
 

@@ -310,6 +310,138 @@ int32_t attn_decode_noalloc(const attn_args *args, void *stream);
 int32_t attn_tree_mask(const int32_t *parent, int32_t n_rows, int32_t prefix_cells, int32_t n_cells,
                        float *mask, int64_t mask_stride_row, void *stream);
 
+/* ---- paged caches ----------------------------------------------------------
+ * A server's K/V cache as a pool of n_pages pages of page_size cells, and one
+ * block table per sequence that names its pages in order: cell c of a
+ * sequence is cell c % page_size of page table[c / page_size], slot
+ * page * page_size + c % page_size of the pool.  Four operations, run one
+ * after the other by a serving step:
+ *   attn_page_tables    takes and returns pages as sequences grow and end, and
+ *                       writes the step's slot map and row ranges;
+ *   attn_append_paged   writes the step's K/V rows through the slot map;
+ *   attn_decode_paged   attention of single rows over their tables;
+ *   attn_decode_shared  the same for groups of rows whose tables begin with
+ *                       the same cells.
+ * They allocate nothing, are asynchronous on `stream` and refuse as the other
+ * operations do.  Sizes are host values; lengths, tables and groups stay on
+ * the device, so that a captured graph replays with new ones. */
+
+enum { ATTN_OP_DECODE_PAGED = 4, ATTN_OP_DECODE_SHARED = 5 };
+
+/* attn_page_tables.  For sequence i with seq_len[i] cells in the cache and
+ * new_len[i] rows in this step:
+ *   new_len >= 0  the sequence grows to seq_len + new_len cells.  It holds
+ *                 ceil(seq_len / page_size) pages; the pages that are missing
+ *                 come from the head of the free ring, in sequence order, and
+ *                 are written into its table row.
+ *   new_len < 0   the sequence ends: its pages from index n_keep[i] on (NULL:
+ *                 0; pages below it are shared with others) go to the tail of
+ *                 the ring, and its length becomes 0.  Its table row stays.
+ * The step's rows are numbered sequence after sequence (seq_row: where each
+ * sequence's rows begin); row t gets its slot, its sequence and the number of
+ * cells it may see, position + 1.  A sequence that cannot grow -- the ring is
+ * empty, the table row is full, its rows pass n_rows -- is left as it was: its
+ * length and table do not change, its rows get slot -1 and row_end 0, and
+ * seq_len_out shows it.  Rows behind the last sequence get slot -1, row_seq -1
+ * and row_end 0.
+ * Table entries and page ids are checked: a length outside [0, table_width *
+ * page_size], an id outside [0, n_pages), a ring state that cannot be, or more
+ * pages returned than the ring holds record ATTN_ERR_INVALID_ARG in the
+ * device status word, and the cells concerned get slot -1.               */
+typedef struct {
+    int32_t n_seqs;             /* 0 .. 16384                                   */
+    int32_t page_size;          /* cells per page, >= 1                         */
+    int32_t n_pages;            /* pages of the pool = entries of the ring; n_pages * page_size < 2^31 */
+    int32_t table_width;        /* entries per table row                        */
+    int32_t n_rows;             /* rows of the step, padding included           */
+    const int32_t *seq_len;     /* [n_seqs]                                     */
+    const int32_t *new_len;     /* [n_seqs]                                     */
+    const int32_t *n_keep;      /* [n_seqs] or NULL                             */
+    int32_t *page_table;        /* [n_seqs][table_width], updated               */
+    int64_t table_stride;       /* entries between table rows (>= table_width)  */
+    int32_t *free_ring;         /* [n_pages], updated at its tail               */
+    const int32_t *free_state;  /* [2]: index of the first free page in the ring, number of free pages */
+    int32_t *free_state_out;    /* [2], not the input array                     */
+    int32_t *slot;              /* [n_rows]                                     */
+    int32_t *row_seq;           /* [n_rows] or NULL                             */
+    int32_t *row_end;           /* [n_rows] or NULL                             */
+    int32_t *seq_row;           /* [n_seqs + 1] or NULL                         */
+    int32_t *seq_len_out;       /* [n_seqs], not the input array                */
+    int32_t reserved[4];        /* must be zero                                 */
+} attn_page_args;
+int32_t attn_page_tables(const attn_page_args *args, void *stream);
+
+/* attn_append_paged: row t of k_new / v_new ([n_rows][n_head_kv][head_dim], in
+ * F32, F16 or BF16) goes to slot[t] of the pool; a row whose slot lies outside
+ * [0, n_pages * page_size) is skipped (padding rows have -1).  The slots of
+ * one call are distinct.  kv_type F16 or BF16: the values, rounded once if
+ * their type differs.  kv_type e4m3 or int8: per row and KV head
+ *   scale = amax / 448 (e4m3) or amax / 127 (int8), rounded to F32, and
+ *   code = the nearest code to x / scale (ties to even; one rounding of the
+ *   exact quotient); scale 0 gives codes of 0; a row with an infinity or NaN
+ *   gets a non-finite scale.
+ * The scales go to k_scale / v_scale[slot * scale_stride_cell + head].
+ * New rows, cache and strides are multiples of 16 bytes.                   */
+typedef struct {
+    int32_t n_rows, n_head_kv, head_dim;     /* head_dim 64, 128 or 256         */
+    int32_t n_pages, page_size;              /* n_pages * page_size < 2^31      */
+    const void *k_new, *v_new; int32_t new_type;
+    int64_t new_stride_row, new_stride_head; /* elements                        */
+    const int32_t *slot;                     /* [n_rows]                        */
+    void *k, *v; int32_t kv_type;
+    int64_t kv_stride_page, kv_stride_cell, kv_stride_head;   /* elements       */
+    float *k_scale, *v_scale; int64_t scale_stride_cell;      /* e4m3 / int8, else NULL */
+    int32_t reserved[4];                     /* must be zero                    */
+} attn_append_args;
+int32_t attn_append_paged(const attn_append_args *args, void *stream);
+
+/* attn_decode_paged / attn_decode_shared.  Row r attends to the cells
+ * [row_begin[r], row_end[r]) of table row_table[r] (NULL: table r), clipped to
+ * [0, table_width * page_size), with the semantics above: softcap, then ALiBi
+ * -slope * |row_end[r] - 1 - c|, sinks; a row that sees no cell is +0.  Cells
+ * outside a row's range never reach it, whatever their pages hold.  Table
+ * entries that no range reaches are not read.  An entry outside [0, n_pages)
+ * inside a range reads as cells of zeros, a row_table entry outside
+ * [0, n_tables) makes its row see nothing, and both record
+ * ATTN_ERR_INVALID_ARG in the device status word.
+ * Types: a 16-bit cache with Q in its dtype, head_dim 64, 128 or 256, up to 16
+ * query heads per KV head; or an e4m3 / int8 cache (scales indexed by slot)
+ * with Q in F16 or BF16, head_dim 128 or 256, up to 8.  Any of F32, F16, BF16
+ * out.  page_size is a multiple of 16; Q is 16-byte aligned with strides that
+ * are multiples of 16 bytes, and so is the cache.
+ * attn_decode_shared: rows group_begin[i] .. group_begin[i + 1] - 1 form group
+ * i, and the first group_len[i] cells of their tables are the same; they are
+ * read once for the group, through the table of its first row, whatever pages
+ * the other rows name there.  Rows of no group run as in attn_decode_paged.
+ * A group_begin that decreases or passes n_rows records ATTN_ERR_INVALID_ARG
+ * and no row is grouped.  Over an e4m3 / int8 cache every row reads its own
+ * table (the same result, nothing shared).                                 */
+typedef struct {
+    int32_t n_rows, n_head_q, n_head_kv, head_dim;
+    int32_t n_pages, page_size;              /* n_pages * page_size < 2^31      */
+    const void *q;   int32_t q_type;   int64_t q_stride_row, q_stride_head;
+    const void *k;   const void *v;    int32_t kv_type;
+    int64_t kv_stride_page, kv_stride_cell, kv_stride_head;   /* elements       */
+    void *out;       int32_t out_type; int64_t o_stride_row, o_stride_head;
+    const int32_t *page_table; int64_t table_stride;          /* [n_tables][table_width] */
+    int32_t n_tables, table_width;           /* table_width * page_size < 2^31  */
+    const int32_t *row_table;                /* [n_rows] or NULL                */
+    const int32_t *row_begin, *row_end;      /* [n_rows]; row_begin may be NULL (0) */
+    int32_t n_groups;                        /* attn_decode_shared, else 0      */
+    const int32_t *group_begin, *group_len;  /* [n_groups + 1], [n_groups]      */
+    float scale, softcap;
+    const float *alibi_slopes, *sinks;       /* [n_head_q] or NULL              */
+    const float *k_scale, *v_scale; int64_t scale_stride_cell;   /* e4m3 / int8: by slot */
+    int32_t reserved[4];                     /* must be zero                    */
+} attn_paged_args;
+
+/* As attn_supports / attn_workspace_size, for ATTN_OP_DECODE_PAGED and
+ * ATTN_OP_DECODE_SHARED.                                                    */
+int32_t attn_paged_supports(const attn_paged_args *args, int32_t op);
+size_t attn_paged_workspace_size(const attn_paged_args *args, int32_t op);
+int32_t attn_decode_paged(const attn_paged_args *args, void *ws, size_t ws_bytes, void *stream);
+int32_t attn_decode_shared(const attn_paged_args *args, void *ws, size_t ws_bytes, void *stream);
+
 /* Synchronizes `stream`, then reads and clears the device status word on the
  * current device: ATTN_OK, or ATTN_ERR_DEVICE_TIMEOUT if a kernel gave up on
  * a bounded wait since the last check.                                      */
