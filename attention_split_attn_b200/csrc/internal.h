@@ -268,6 +268,40 @@ int paged_stream_warps(int kv_type, int D, int G, int sms);
 cudaError_t launch_paged_stream(const PagedPlan& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                 cudaStream_t stream);
 
+// Shared prefixes (attn_decode_shared): a block is up to n_slot tiles of rpt
+// rows (rpt x G <= 128 lanes) of one group.
+struct SharedBlock {
+  int32_t row0, n_rows;
+  int32_t table, len;      // the group's table (its first row's) and shared cells
+  int32_t lo, hi;          // cells [lo, hi) of the shared ones that some row of the block sees
+  int32_t kt0, nt;         // the 128-cell tiles that hold them
+  int32_t w;               // work per tile: 2 when both slots hold rows, else 1
+  int32_t clo[2], chi[2];  // cells that every row of a slot sees (rows that see none left out)
+};
+struct SharedPlan {
+  PagedPlan p;             // own_lo NULL: whole ranges
+  int32_t n_groups;
+  const int32_t *group_begin, *group_len;
+  int32_t n_slot, rpt, block_rows;
+  SharedBlock* blocks;     // workspace [max blocks]
+  int64_t* blk_off;        // workspace [max blocks + 1]: exclusive prefix of nt * w
+  int32_t* n_blk;          // workspace [1]
+  int32_t* row_blk;        // workspace [R]: the row's block or -1
+  int32_t* own_lo;         // workspace [R]: first cell of the row's own part
+  float *rec_o, *rec_ml;   // workspace records: [R][Hq], then [W][256]; [D] and [2] floats each
+  int32_t W;               // CTAs of the persistent grid
+  int32_t box_cells;       // cells per TMA box: the largest power of 2 <= 128 that divides P
+  float scale2;            // scale log2(e)
+  float s_lim, c3, c5, c7, c9;   // softcap series in the raw product (s_lim 0: not usable)
+  int32_t plain;           // no softcap, no ALiBi, scale > 0
+  int32_t out_vec;         // output rows may be written with 16-byte stores
+};
+cudaError_t launch_shared(const SharedPlan& sp, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                          cudaStream_t stream);
+// Folds the shared pieces' records, the own parts' (p with own_lo, its W and
+// records) and the sinks.
+cudaError_t launch_shared_combine(const SharedPlan& sp, const PagedPlan& own, cudaStream_t stream);
+
 // Block tables and slot maps from sequence lengths (fields as in attn_page_args).
 struct PageTablesPlan {
   attn_page_args a;

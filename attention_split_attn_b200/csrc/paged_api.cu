@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -210,6 +211,35 @@ PagedWs paged_ws(const attn_paged_args* a, int W) {
   return w;
 }
 
+// What decode_shared adds: the plan (blocks of rows, their work prefix, each
+// row's block and own first cell) and the shared pieces' records: a home record
+// per (row, q head) and 256 lanes per run.
+struct SharedWs {
+  size_t blocks_off, off_off, n_off, blk_off, own_off, o_off, ml_off, total;
+};
+int shared_slots(int D) { return D <= 128 ? 2 : 1; }
+int64_t shared_block_rows(const attn_paged_args* a) {
+  return (int64_t)shared_slots(a->head_dim) * (128 / (a->n_head_q / a->n_head_kv));
+}
+bool runs_shared(const attn_paged_args* a, int32_t op) {
+  return op == ATTN_OP_DECODE_SHARED && is16(a->kv_type) && a->n_groups > 0 && a->n_pages > 0;
+}
+SharedWs shared_ws(const attn_paged_args* a, size_t base, int sms) {
+  SharedWs w{};
+  const size_t R = (size_t)a->n_rows;
+  const size_t nb = (size_t)std::min(a->n_groups, a->n_rows) + R / (size_t)shared_block_rows(a) + 1;
+  w.blocks_off = align256(base);
+  w.off_off = w.blocks_off + align256(nb * sizeof(SharedBlock));
+  w.n_off = w.off_off + align256((nb + 1) * sizeof(int64_t));
+  w.blk_off = w.n_off + 256;
+  w.own_off = w.blk_off + align256(R * sizeof(int32_t));
+  w.o_off = w.own_off + align256(R * sizeof(int32_t));
+  const size_t records = R * a->n_head_q + (size_t)sms * 256;
+  w.ml_off = w.o_off + align256(records * a->head_dim * sizeof(float));
+  w.total = w.ml_off + align256(records * 2 * sizeof(float));
+  return w;
+}
+
 // The pool as a 4-D map [page][cell][head][D] with boxes of 128 bytes of one
 // head of box_cells cells of a page.
 int32_t pool_map(CUtensorMap* map, const void* base, const attn_paged_args* a, int box_cells) {
@@ -246,6 +276,55 @@ void fill_plan(PagedPlan* p, const attn_paged_args* a, const PagedWs& wl, char* 
   p->row_table = a->row_table;
 }
 
+// The plan of the shared part (the softcap's series as in api.cu: the odd
+// Taylor terms of c tanh(scale s / c) in the raw product s, times log2(e)).
+void fill_shared(SharedPlan* sp, const PagedPlan& p, const attn_paged_args* a, const SharedWs& w, char* ws, int sms) {
+  memset(sp, 0, sizeof(*sp));
+  sp->p = p;
+  sp->p.own_lo = nullptr;
+  sp->n_groups = a->n_groups;
+  sp->group_begin = a->group_begin; sp->group_len = a->group_len;
+  sp->n_slot = shared_slots(a->head_dim);
+  sp->rpt = 128 / p.d.G;
+  sp->block_rows = (int32_t)shared_block_rows(a);
+  sp->blocks = reinterpret_cast<SharedBlock*>(ws + w.blocks_off);
+  sp->blk_off = reinterpret_cast<int64_t*>(ws + w.off_off);
+  sp->n_blk = reinterpret_cast<int32_t*>(ws + w.n_off);
+  sp->row_blk = reinterpret_cast<int32_t*>(ws + w.blk_off);
+  sp->own_lo = reinterpret_cast<int32_t*>(ws + w.own_off);
+  sp->rec_o = reinterpret_cast<float*>(ws + w.o_off);
+  sp->rec_ml = reinterpret_cast<float*>(ws + w.ml_off);
+  sp->W = sms;
+  sp->box_cells = 16;
+  while (sp->box_cells < 128 && a->page_size % (2 * sp->box_cells) == 0) sp->box_cells *= 2;
+  const double L2E = 1.4426950408889634, sc = a->scale, c = a->softcap;
+  sp->scale2 = (float)(sc * L2E);
+  sp->plain = !(a->softcap > 0.f) && !a->alibi_slopes && sp->scale2 > 1e-30f && sp->scale2 < 1e30f;
+  if (a->softcap > 0.f) {
+    const double s2 = sc * sc / (c * c);
+    const double c3 = -1.0 / 3.0 * sc * s2 * L2E, c5 = 2.0 / 15.0 * sc * s2 * s2 * L2E;
+    const double c7 = -17.0 / 315.0 * sc * s2 * s2 * s2 * L2E, c9 = 62.0 / 2835.0 * sc * s2 * s2 * s2 * s2 * L2E;
+    const double lim = 0.4 * c / std::fabs(sc);
+    auto normal = [](double v) { return std::fabs(v) >= 1.1754943508222875e-38 && std::fabs(v) <= 3.0e38; };
+    if (normal(sc) && normal(c3) && normal(c5) && normal(c7) && normal(c9) && normal(lim) && normal(lim * lim)) {
+      sp->c3 = (float)c3; sp->c5 = (float)c5; sp->c7 = (float)c7; sp->c9 = (float)c9;
+      sp->s_lim = (float)lim;
+    }
+  }
+  const int64_t ovec = 16 / esize(a->out_type);
+  sp->out_vec = aligned16(a->out) && (a->n_rows <= 1 || a->o_stride_row % ovec == 0) &&
+                (a->n_head_q <= 1 || a->o_stride_head % ovec == 0);
+}
+
+// Q as [rows][heads][D] with boxes of 128 / G rows of the G heads of a KV head.
+int32_t q_map(CUtensorMap* map, const attn_paged_args* a, int G) {
+  const int D = a->head_dim;
+  const int64_t dims[3] = {D, a->n_head_q, a->n_rows};
+  const int64_t strides[2] = {(a->n_head_q > 1 ? a->q_stride_head : D) * 2, (a->n_rows > 1 ? a->q_stride_row : D) * 2};
+  const int32_t box[3] = {64, G, 128 / G};
+  return encode_map(map, a->q, a->q_type, 3, dims, strides, box);
+}
+
 int32_t run_paged(const attn_paged_args* a, int32_t op, void* ws, size_t ws_bytes, void* stream) {
   int32_t st = check_paged(a, op);
   if (st != ATTN_OK) return st;
@@ -254,8 +333,11 @@ int32_t run_paged(const attn_paged_args* a, int32_t op, void* ws, size_t ws_byte
   if ((st = device_facts(&sms, &status)) != ATTN_OK) return st;
   const int W = paged_stream_warps(a->kv_type, a->head_dim, a->n_head_q / a->n_head_kv, sms);
   const PagedWs wl = paged_ws(a, W);
-  if (ws == nullptr || ws_bytes < wl.total)
-    return refuse(ATTN_ERR_WORKSPACE, "paged decode needs %zu workspace bytes, got %zu", wl.total, ws_bytes);
+  const bool shared = runs_shared(a, op);
+  const SharedWs sw = shared ? shared_ws(a, wl.total, sms) : SharedWs{};
+  const size_t need = shared ? sw.total : wl.total;
+  if (ws == nullptr || ws_bytes < need)
+    return refuse(ATTN_ERR_WORKSPACE, "paged decode needs %zu workspace bytes, got %zu", need, ws_bytes);
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return refuse(ATTN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
   CUtensorMap tmK, tmV;
   memset(&tmK, 0, sizeof(tmK));
@@ -269,7 +351,25 @@ int32_t run_paged(const attn_paged_args* a, int32_t op, void* ws, size_t ws_byte
     p.width = 0;   // no pages: every range is empty
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_paged_stream(p, tmK, tmV, s);
+  cudaError_t e;
+  if (shared) {
+    SharedPlan sp;
+    fill_shared(&sp, p, a, sw, static_cast<char*>(ws), sms);
+    CUtensorMap tmQ, sK, sV;
+    if ((st = q_map(&tmQ, a, p.d.G)) != ATTN_OK) return st;
+    if ((st = pool_map(&sK, a->k, a, sp.box_cells)) != ATTN_OK) return st;
+    if ((st = pool_map(&sV, a->v, a, sp.box_cells)) != ATTN_OK) return st;
+    if ((e = launch_shared(sp, tmQ, sK, sV, s)) != cudaSuccess)
+      return refuse(ATTN_ERR_CUDA, "shared decode launch: %s", cudaGetErrorString(e));
+    p.own_lo = sp.own_lo;       // the stream kernel takes the rows' own cells, planned above
+    p.d.plan_inline = 0;
+    if ((e = launch_paged_stream(p, tmK, tmV, s)) != cudaSuccess)
+      return refuse(ATTN_ERR_CUDA, "paged decode launch: %s", cudaGetErrorString(e));
+    if ((e = launch_shared_combine(sp, p, s)) != cudaSuccess)
+      return refuse(ATTN_ERR_CUDA, "combine launch: %s", cudaGetErrorString(e));
+    return ATTN_OK;
+  }
+  e = launch_paged_stream(p, tmK, tmV, s);
   if (e != cudaSuccess) return refuse(ATTN_ERR_CUDA, "paged decode launch: %s", cudaGetErrorString(e));
   CombinePlan cp{};
   cp.R = a->n_rows; cp.Hq = a->n_head_q; cp.Hkv = a->n_head_kv; cp.G = p.d.G; cp.D = a->head_dim;
@@ -317,7 +417,8 @@ size_t attn_paged_workspace_size(const attn_paged_args* a, int32_t op) {
   if (check_paged(a, op) != ATTN_OK || a->n_rows == 0) return 0;
   int sms = 148, *status = nullptr;
   device_facts(&sms, &status);
-  return paged_ws(a, paged_stream_warps(a->kv_type, a->head_dim, a->n_head_q / a->n_head_kv, sms)).total;
+  const size_t n = paged_ws(a, paged_stream_warps(a->kv_type, a->head_dim, a->n_head_q / a->n_head_kv, sms)).total;
+  return runs_shared(a, op) ? shared_ws(a, n, sms).total : n;
 }
 
 int32_t attn_decode_paged(const attn_paged_args* a, void* ws, size_t ws_bytes, void* stream) {

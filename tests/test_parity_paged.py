@@ -535,6 +535,16 @@ def test_shared_edges(cuda_lib):
     check(Case(26, ends, P=16, Hq=4, Hkv=2, D=64, begins=begins), A.OP_DECODE_SHARED)   # no groups given
 
 
+@pytest.mark.parametrize("begin", [[0, 5, 3], [0, 2, 9], [-1, 2, 4]])
+def test_shared_groups_that_cannot_be(cuda_lib, begin):
+    c = Case(27, [100, 120, 90, 99], P=16, Hq=4, Hkv=2, D=64, groups=[(2, 64), (2, 32)])
+    c.groups["group_begin"] = i32(begin)
+    got = c.run(A.OP_DECODE_SHARED)
+    with pytest.raises(A.AttnError, match="INVALID_ARG"):
+        A.check_device_status()
+    compare(got, c.expected(), 1e-5, 2e-2)
+
+
 @pytest.mark.parametrize("cache", ["e4m3", "i8"])
 def test_shared_one_byte(cuda_lib, cache):
     check(Case(28, [300, 301, 450, 299], D=128, P=16, cache=cache, groups=[(4, 299)]), A.OP_DECODE_SHARED)
