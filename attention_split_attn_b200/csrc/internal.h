@@ -278,14 +278,22 @@ struct SharedBlock {
   int32_t w;               // work per tile: 2 when both slots hold rows, else 1
   int32_t clo[2], chi[2];  // cells that every row of a slot sees (rows that see none left out)
 };
+// Where a run of the persistent grid begins: tile i of block k, KV head g
+// (tile 0 is the unit's last cell tile).  Run w ends where run w + 1 begins.
+struct SharedRun {
+  int32_t k, g, i, pad;
+  SharedBlock b;           // block k (unset behind the last)
+};
 struct SharedPlan {
   PagedPlan p;             // own_lo NULL: whole ranges
   int32_t n_groups;
   const int32_t *group_begin, *group_len;
   int32_t n_slot, rpt, block_rows;
   SharedBlock* blocks;     // workspace [max blocks]
-  int64_t* blk_off;        // workspace [max blocks + 1]: exclusive prefix of nt * w
-  int32_t* n_blk;          // workspace [1]
+  int64_t* blk_off;        // workspace [max blocks + 1]: the planner's work prefix when shared memory cannot hold it
+  int32_t max_blk;
+  SharedRun* runs;         // workspace [W + 1]
+  int2* unit_runs;         // workspace [max blocks][Hkv]: first and last run of the unit
   int32_t* row_blk;        // workspace [R]: the row's block or -1
   int32_t* own_lo;         // workspace [R]: first cell of the row's own part
   float *rec_o, *rec_ml;   // workspace records: [R][Hq], then [W][256]; [D] and [2] floats each
@@ -298,9 +306,9 @@ struct SharedPlan {
 };
 cudaError_t launch_shared(const SharedPlan& sp, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                           cudaStream_t stream);
-// Folds the shared pieces' records, the own parts' (p with own_lo, its W and
-// records) and the sinks.
-cudaError_t launch_shared_combine(const SharedPlan& sp, const PagedPlan& own, cudaStream_t stream);
+// Folds the own parts' records (`own`: its W, row_tiles and records), those of
+// the shared pieces (sp, or NULL) and the sinks.
+cudaError_t launch_paged_combine(const SharedPlan* sp, const PagedPlan& own, int sms, cudaStream_t stream);
 
 // Block tables and slot maps from sequence lengths (fields as in attn_page_args).
 struct PageTablesPlan {

@@ -191,7 +191,7 @@ int32_t check_paged(const attn_paged_args* a, int32_t op_id) {
     return refuse(ATTN_ERR_UNSUPPORTED, "%s: Q must be 16-byte aligned with strides that are multiples of 8", op);
   if (shared && ((a->n_rows > 1 && a->q_stride_row == 0) || (a->n_head_q > 1 && a->q_stride_head == 0)))
     return refuse(ATTN_ERR_UNSUPPORTED, "%s: zero q stride", op);
-  if ((int64_t)a->n_rows * a->n_head_q * 32 > 0x7fffffffLL * 128)
+  if ((int64_t)a->n_rows * a->n_head_q > 0x7fffffffLL)
     return refuse(ATTN_ERR_UNSUPPORTED, "%s: too many rows", op);
   return ATTN_OK;
 }
@@ -215,23 +215,34 @@ PagedWs paged_ws(const attn_paged_args* a, int W) {
 // row's block and own first cell) and the shared pieces' records: a home record
 // per (row, q head) and 256 lanes per run.
 struct SharedWs {
-  size_t blocks_off, off_off, n_off, blk_off, own_off, o_off, ml_off, total;
+  size_t blocks_off, off_off, runs_off, unit_off, blk_off, own_off, o_off, ml_off, total;
 };
 int shared_slots(int D) { return D <= 128 ? 2 : 1; }
 int64_t shared_block_rows(const attn_paged_args* a) {
   return (int64_t)shared_slots(a->head_dim) * (128 / (a->n_head_q / a->n_head_kv));
 }
+// Sharing takes four launches and a plan, about 10 us more than row by row,
+// and saves at most the reading of all rows' tables.  Below 64 MB of them (at
+// 5.4 TB/s 12 us) row by row is the faster form whatever the groups: 8 rows
+// of 1100 cells, 8 KV heads, D 128 (38 MB) take 16 us against 25 us.
+constexpr int64_t kShareBytes = 64LL << 20;
 bool runs_shared(const attn_paged_args* a, int32_t op) {
-  return op == ATTN_OP_DECODE_SHARED && is16(a->kv_type) && a->n_groups > 0 && a->n_pages > 0;
+  if (op != ATTN_OP_DECODE_SHARED || !is16(a->kv_type) || a->n_groups == 0 || a->n_pages == 0) return false;
+  const double bytes = (double)a->n_rows * a->n_head_kv * a->table_width * a->page_size * 4.0 * a->head_dim;
+  return bytes > (double)kShareBytes;
+}
+size_t shared_max_blocks(const attn_paged_args* a) {
+  return (size_t)std::min(a->n_groups, a->n_rows) + (size_t)a->n_rows / (size_t)shared_block_rows(a) + 1;
 }
 SharedWs shared_ws(const attn_paged_args* a, size_t base, int sms) {
   SharedWs w{};
   const size_t R = (size_t)a->n_rows;
-  const size_t nb = (size_t)std::min(a->n_groups, a->n_rows) + R / (size_t)shared_block_rows(a) + 1;
+  const size_t nb = shared_max_blocks(a);
   w.blocks_off = align256(base);
   w.off_off = w.blocks_off + align256(nb * sizeof(SharedBlock));
-  w.n_off = w.off_off + align256((nb + 1) * sizeof(int64_t));
-  w.blk_off = w.n_off + 256;
+  w.runs_off = w.off_off + align256((nb + 1) * sizeof(int64_t));
+  w.unit_off = w.runs_off + align256(((size_t)sms + 1) * sizeof(SharedRun));
+  w.blk_off = w.unit_off + align256(nb * a->n_head_kv * sizeof(int2));
   w.own_off = w.blk_off + align256(R * sizeof(int32_t));
   w.o_off = w.own_off + align256(R * sizeof(int32_t));
   const size_t records = R * a->n_head_q + (size_t)sms * 256;
@@ -289,7 +300,9 @@ void fill_shared(SharedPlan* sp, const PagedPlan& p, const attn_paged_args* a, c
   sp->block_rows = (int32_t)shared_block_rows(a);
   sp->blocks = reinterpret_cast<SharedBlock*>(ws + w.blocks_off);
   sp->blk_off = reinterpret_cast<int64_t*>(ws + w.off_off);
-  sp->n_blk = reinterpret_cast<int32_t*>(ws + w.n_off);
+  sp->max_blk = (int32_t)shared_max_blocks(a);
+  sp->runs = reinterpret_cast<SharedRun*>(ws + w.runs_off);
+  sp->unit_runs = reinterpret_cast<int2*>(ws + w.unit_off);
   sp->row_blk = reinterpret_cast<int32_t*>(ws + w.blk_off);
   sp->own_lo = reinterpret_cast<int32_t*>(ws + w.own_off);
   sp->rec_o = reinterpret_cast<float*>(ws + w.o_off);
@@ -365,19 +378,13 @@ int32_t run_paged(const attn_paged_args* a, int32_t op, void* ws, size_t ws_byte
     p.d.plan_inline = 0;
     if ((e = launch_paged_stream(p, tmK, tmV, s)) != cudaSuccess)
       return refuse(ATTN_ERR_CUDA, "paged decode launch: %s", cudaGetErrorString(e));
-    if ((e = launch_shared_combine(sp, p, s)) != cudaSuccess)
+    if ((e = launch_paged_combine(&sp, p, sms, s)) != cudaSuccess)
       return refuse(ATTN_ERR_CUDA, "combine launch: %s", cudaGetErrorString(e));
     return ATTN_OK;
   }
   e = launch_paged_stream(p, tmK, tmV, s);
   if (e != cudaSuccess) return refuse(ATTN_ERR_CUDA, "paged decode launch: %s", cudaGetErrorString(e));
-  CombinePlan cp{};
-  cp.R = a->n_rows; cp.Hq = a->n_head_q; cp.Hkv = a->n_head_kv; cp.G = p.d.G; cp.D = a->head_dim;
-  cp.out = p.d.out; cp.sinks = a->sinks; cp.part = p.d.part;
-  cp.mode = 1;
-  cp.row_tiles = p.d.row_tiles; cp.W = W;
-  cp.use_pdl = 1;
-  e = launch_combine(cp, s);
+  e = launch_paged_combine(nullptr, p, sms, s);
   if (e != cudaSuccess) return refuse(ATTN_ERR_CUDA, "combine launch: %s", cudaGetErrorString(e));
   return ATTN_OK;
 }

@@ -15,7 +15,7 @@
 // at head dim 128 (2048 cycles of each per pair of 128 x 128 tiles) and ahead
 // of them at 64.
 //
-// Three kernels:
+// Kernels:
 //  * shared_plan_kernel (one CTA) checks the groups, cuts their rows into
 //    blocks (up to two tiles of 128 / G rows x G heads), and writes each block's cell
 //    range and tile count, the prefix of the blocks' work, every row's block and
@@ -37,9 +37,9 @@
 //    and the odd ones on slot 1 (each K/V tile used once), so that one slot's
 //    products run under the other's softmax in both cases.  At head dim 256
 //    tensor memory holds one slot.
-//  * shared_combine_kernel folds, per (row, query head), the pieces' records,
-//    the own part's records and the sink.  A row whose cells were all seen by
-//    one piece is finished by that piece and skipped here.
+//  * the combine (paged_combine.cu) folds, per (row, query head), the pieces'
+//    records, the own part's records and the sink.  A row whose cells were all
+//    seen by one piece is finished by that piece and skipped there.
 //
 // Cells that a row must not see never reach it: their weight is an exact 0,
 // V rows outside the block's range are zeroed in shared memory, and a tile that
@@ -148,8 +148,13 @@ __device__ __forceinline__ uint32_t ring_phase(int64_t i) { return (uint32_t)((i
 // planner
 // ---------------------------------------------------------------------------
 
-// Exclusive scan of x over the CTA's 1024 threads on top of *carry (the same
-// in every thread), which grows by the total.
+// One CTA: everything between its loads and its stores happens in shared
+// memory, so its time is a few dependent loads and barriers.
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanBlocks = 1024;   // blocks kept in shared memory; a plan that may hold more works in the workspace
+
+// Exclusive scan of x over the CTA on top of *carry (the same in every
+// thread), which grows by the total.
 __device__ __forceinline__ int64_t cta_excl_scan(int64_t x, int64_t* carry, long long* wsum) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   int64_t v = x;
@@ -161,41 +166,57 @@ __device__ __forceinline__ int64_t cta_excl_scan(int64_t x, int64_t* carry, long
   __syncthreads();   // the previous scan's sums are read
   if (lane == 31) wsum[wid] = v;
   __syncthreads();
-  int64_t before = 0, total = 0;
-  for (int k = 0; k < 32; ++k) {
-    const int64_t s = wsum[k];
-    if (k < wid) before += s;
-    total += s;
+  int64_t s = wsum[lane];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, s, off);
+    if (lane >= off) s += y;
   }
-  const int64_t excl = *carry + before + v - x;
-  *carry += total;
+  const int64_t before = __shfl_sync(0xffffffffu, s, wid > 0 ? wid - 1 : 0);
+  const int64_t excl = *carry + (wid > 0 ? before : 0) + v - x;
+  *carry += __shfl_sync(0xffffffffu, s, 31);
   return excl;
 }
 
-__global__ void __launch_bounds__(1024) shared_plan_kernel(const SharedPlan sp) {
+struct PlanShared {
+  SharedBlock blocks[kPlanBlocks];
+  int64_t off[kPlanBlocks + 1];
+  int first_run[kPlanBlocks + 1];   // when units <= W
+  long long wsum[32];
+};
+
+// Dynamic shared memory: PlanShared, or only its wsum when the blocks and
+// their offsets live in the workspace.
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedPlan sp) {
+  extern __shared__ long long plan_smem[];
   pdl_launch_dependents();
   pdl_wait_prior_grid();
-  __shared__ long long wsum[32];
   const PagedPlan& p = sp.p;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = p.d.R;
-  // 1. groups that are well formed, rows without a group
+  const int tid = threadIdx.x, R = p.d.R, Hkv = p.d.Hkv;
+  const bool in_smem = sp.max_blk <= kPlanBlocks;
+  PlanShared* ps = reinterpret_cast<PlanShared*>(plan_smem);
+  SharedBlock* blocks = in_smem ? ps->blocks : sp.blocks;
+  int64_t* off = in_smem ? ps->off : sp.blk_off;
+  long long* wsum = in_smem ? ps->wsum : plan_smem;
+
+  // the first rows' ranges and the groups are loaded together: one latency
+  PagedRow first_row{};
+  if (tid < R) first_row = paged_row(p, tid);   // (own_lo of this plan is NULL: the whole range)
+
+  // 1. are the groups well formed?
   bool bad = false;
-  for (int i = tid; i <= sp.n_groups; i += 1024) {
+  for (int i = tid; i <= sp.n_groups; i += kPlanThreads) {
     const int b = __ldg(sp.group_begin + i);
     bad |= b < 0 || b > R || (i > 0 && b < __ldg(sp.group_begin + i - 1));
   }
   const bool any_bad = __syncthreads_or(bad);
   if (any_bad && tid == 0) record_status(p.d.status, ATTN_ERR_INVALID_ARG);
   const int n_groups = any_bad ? 0 : sp.n_groups;
-  for (int r = tid; r < R; r += 1024) {
-    sp.row_blk[r] = -1;
-    sp.own_lo[r] = 0;
-  }
-  __syncthreads();
+
   // 2. blocks of at most block_rows rows (a group of one row shares nothing)
   const int cap = p.width * p.P;
-  int64_t n_blk = 0;
-  for (int base = 0; base < n_groups; base += 1024) {
+  int64_t nb = 0;
+  for (int base = 0; base < n_groups; base += kPlanThreads) {
     const int i = base + tid;
     int r0 = 0, n = 0, len = 0, table = 0;
     if (i < n_groups) {
@@ -206,92 +227,196 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const SharedPlan sp) 
       if (n < 2 || len <= 0 || table < 0 || table >= p.n_tables) n = 0;
     }
     const int mine = (n + sp.block_rows - 1) / sp.block_rows;
-    const int64_t at = cta_excl_scan(mine, &n_blk, wsum);
+    const int64_t at = cta_excl_scan(mine, &nb, wsum);
     for (int k = 0; k < mine; ++k) {
       SharedBlock b;
       b.row0 = r0 + k * sp.block_rows;
       b.n_rows = min(sp.block_rows, n - k * sp.block_rows);
       b.table = table;
       b.len = len;
-      sp.blocks[at + k] = b;
+      b.lo = 0x7fffffff;
+      b.hi = 0;
+      b.w = (sp.n_slot == 2 && b.n_rows > sp.rpt) ? 2 : 1;
+      b.kt0 = b.nt = 0;
+      b.clo[0] = b.clo[1] = 0;
+      b.chi[0] = b.chi[1] = 0x7fffffff;
+      blocks[at + k] = b;
     }
   }
+  const int n_blk = (int)nb;
   __syncthreads();
-  // 3. each block's cell range: a warp per block
-  for (int64_t k = warp; k < n_blk; k += 32) {
-    SharedBlock b = sp.blocks[k];
-    int lo = 0x7fffffff, hi = 0, clo[2] = {0, 0}, chi[2] = {0x7fffffff, 0x7fffffff};
-    const bool two = sp.n_slot == 2 && b.n_rows > sp.rpt;
-    for (int j = lane; j < b.n_rows; j += 32) {
-      const int r = b.row0 + j;
-      const PagedRow row = paged_row(p, r);   // (own_lo of this plan is NULL: the whole range)
-      const int e = min(row.end, b.len);
-      if (e > row.begin) {
-        lo = min(lo, row.begin);
-        hi = max(hi, e);
-        const int s = two && j >= sp.rpt ? 1 : 0;
-        clo[s] = max(clo[s], row.begin);
-        chi[s] = min(chi[s], e);
-      }
-      sp.row_blk[r] = (int)k;
-      sp.own_lo[r] = b.len;
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    for (int s = 0; s < 2; ++s) {
-      clo[s] = __reduce_max_sync(0xffffffffu, clo[s]);
-      chi[s] = __reduce_min_sync(0xffffffffu, chi[s]);
-    }
-    if (lane == 0) {
-      b.lo = min(lo, hi);
-      b.hi = hi;
-      b.kt0 = b.lo / kShCells;
-      b.nt = hi > b.lo ? (hi + kShCells - 1) / kShCells - b.kt0 : 0;
-      b.w = two ? 2 : 1;
-      for (int s = 0; s < 2; ++s) {
-        b.clo[s] = clo[two ? s : 0];
-        b.chi[s] = chi[two ? s : 0];
-      }
-      sp.blocks[k] = b;
-    }
-  }
-  __syncthreads();
-  // 4. prefix of the blocks' work, in tiles of one slot
+
+  // 3. rows: their block, its cell range, and the own parts' tile prefix
   int64_t carry = 0;
-  for (int64_t base = 0; base < n_blk; base += 1024) {
-    const int64_t k = base + tid;
-    const int64_t x = k < n_blk ? (int64_t)sp.blocks[k].nt * sp.blocks[k].w : 0;
-    const int64_t at = cta_excl_scan(x, &carry, wsum);
-    if (k < n_blk) sp.blk_off[k] = at;
-  }
-  if (tid == 0) {
-    sp.blk_off[n_blk] = carry;
-    *sp.n_blk = (int)n_blk;
-  }
-  // 5. prefix of the own parts' 16-cell tiles
-  carry = 0;
-  for (int base = 0; base < R; base += 1024) {
+  for (int base = 0; base < R; base += kPlanThreads) {
     const int r = base + tid;
-    int64_t x = 0;
+    int64_t tiles = 0;
     if (r < R) {
-      PagedRow row = paged_row(p, r);
-      row.begin = max(row.begin, sp.own_lo[r]);
+      PagedRow row = base == 0 ? first_row : paged_row(p, r);
+      int k = -1, own = 0;
+      {   // the last block with row0 <= r
+        int lo = 0, hi = n_blk;
+        while (hi - lo > 0) {
+          const int mid = (lo + hi) >> 1;
+          if (blocks[mid].row0 <= r) lo = mid + 1;
+          else hi = mid;
+        }
+        if (lo > 0 && r < blocks[lo - 1].row0 + blocks[lo - 1].n_rows) k = lo - 1;
+      }
+      if (k >= 0) {
+        SharedBlock* b = blocks + k;
+        own = b->len;
+        const int e = min(row.end, own);
+        if (e > row.begin) {
+          const int s = b->w == 2 && r - b->row0 >= sp.rpt ? 1 : 0;
+          atomicMin(&b->lo, row.begin);
+          atomicMax(&b->hi, e);
+          atomicMax(&b->clo[s], row.begin);
+          atomicMin(&b->chi[s], e);
+        }
+      }
+      sp.row_blk[r] = k;
+      sp.own_lo[r] = own;
+      row.begin = max(row.begin, own);
       row.end = max(row.end, row.begin);
       row.tile0 = row.begin / 16;
-      x = row.tiles();
+      tiles = row.tiles();
     }
-    const int64_t at = cta_excl_scan(x, &carry, wsum);
+    const int64_t at = cta_excl_scan(tiles, &carry, wsum);
     if (r < R) p.d.row_tiles[r] = at;
   }
   if (tid == 0) p.d.row_tiles[R] = carry;
+  __syncthreads();
+
+  // 4. the blocks' tiles, and the prefix of their work in tiles of one slot
+  int64_t work = 0;
+  for (int base = 0; base < n_blk; base += kPlanThreads) {
+    const int k = base + tid;
+    int64_t x = 0;
+    if (k < n_blk) {
+      SharedBlock b = blocks[k];
+      if (!in_smem) {   // updated by atomics: read past the L1 cache
+        b.lo = __ldcg(&blocks[k].lo);
+        b.hi = __ldcg(&blocks[k].hi);
+        for (int s = 0; s < 2; ++s) {
+          b.clo[s] = __ldcg(&blocks[k].clo[s]);
+          b.chi[s] = __ldcg(&blocks[k].chi[s]);
+        }
+      }
+      b.lo = min(b.lo, b.hi);
+      b.kt0 = b.lo / kShCells;
+      b.nt = b.hi > b.lo ? (b.hi + kShCells - 1) / kShCells - b.kt0 : 0;
+      if (b.w == 1) {   // one tile of rows: both slots work on it
+        b.clo[1] = b.clo[0];
+        b.chi[1] = b.chi[0];
+      }
+      blocks[k] = b;
+      if (in_smem) sp.blocks[k] = b;
+      x = (int64_t)b.nt * b.w;
+    }
+    const int64_t at = cta_excl_scan(x, &work, wsum);
+    if (k < n_blk) off[k] = at;
+  }
+  if (tid == 0) off[n_blk] = work;
+  __syncthreads();
+
+  // 5. runs.  Units (block, KV head) that outnumber the runs: equal runs of
+  // the flattened work, wherever their ends fall.  Fewer units: every unit
+  // gets runs of its own, in proportion to its work, so that a run sets up and
+  // writes out one piece only (a piece costs about as much as two tiles) --
+  // while runs are short: rounding to whole runs leaves them uneven, by 20% and
+  // more for a few units of different lengths.
+  const int W = sp.W;
+  const int64_t T = work * Hkv;
+  const bool parts = in_smem && (int64_t)n_blk * Hkv <= W && T > 0 && T <= 16 * W;
+  const SharedRun none{n_blk, 0, 0, 0, {}};
+  if (!parts) {
+    for (int w = tid; w <= W; w += kPlanThreads) {
+      SharedRun s = none;
+      const int64_t t = div64(T * w, W);
+      if (t < T) {
+        int lo = 0, hi = n_blk;   // the last block whose work starts at or before t
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (Hkv * off[mid] <= t) lo = mid;
+          else hi = mid;
+        }
+        const int bw = blocks[lo].w, nt = blocks[lo].nt;
+        const int64_t in = t - Hkv * off[lo], unit = (int64_t)nt * bw;   // (the last such block has work)
+        s.k = lo;
+        s.g = (int)div64(in, unit);
+        s.i = (int)((in - s.g * unit + bw - 1) / bw);
+        if (s.i == nt) {   // the unit's end: the start of the next unit with a tile
+          s.i = 0;
+          if (++s.g == Hkv) {
+            s.g = 0;
+            do ++s.k;
+            while (s.k < n_blk && blocks[s.k].nt == 0);
+          }
+        }
+        if (s.k < n_blk) s.b = blocks[s.k];
+      }
+      sp.runs[w] = s;
+    }
+    for (int64_t base = 0; base < (int64_t)n_blk * Hkv; base += kPlanThreads) {
+      const int64_t u = base + tid;
+      int2 v = make_int2(0, -1);
+      if (u < (int64_t)n_blk * Hkv) {
+        const int k = (int)div64(u, Hkv), g = (int)(u - (int64_t)k * Hkv);
+        const SharedBlock& b = blocks[k];
+        if (b.nt > 0) {
+          const int64_t at = Hkv * off[k] + (int64_t)g * b.nt * b.w, last = at + (int64_t)(b.nt - 1) * b.w;
+          v = make_int2(run_of(at, T, W), run_of(last, T, W));
+        }
+      }
+      if (u < (int64_t)n_blk * Hkv) sp.unit_runs[u] = v;
+    }
+  } else {
+    // units <= W: their first runs, kept in shared memory (the scan's order)
+    const int units = n_blk * Hkv;
+    int64_t used = 0;
+    int* first_run = ps->first_run;
+    for (int base = 0; base < units; base += kPlanThreads) {
+      const int u = base + tid;
+      int n = 0;
+      if (u < units) {
+        const SharedBlock& b = blocks[u / Hkv];
+        // floor(share of the runs beyond one each) + 1, at most one per tile
+        if (b.nt > 0) n = min(b.nt, 1 + (int)div64((int64_t)b.nt * b.w * (W - units), T));
+      }
+      const int64_t at = cta_excl_scan(n, &used, wsum);
+      if (u < units) {
+        first_run[u] = (int)at;
+        sp.unit_runs[u] = make_int2((int)at, (int)at + n - 1);
+      }
+    }
+    if (tid == 0) first_run[units] = (int)used;
+    __syncthreads();
+    for (int w = tid; w <= W; w += kPlanThreads) {
+      SharedRun s = none;
+      if (w < used) {
+        int lo = 0, hi = units;   // the last unit whose first run is at or before w
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (first_run[mid] <= w) lo = mid;
+          else hi = mid;
+        }
+        s.k = lo / Hkv;
+        s.g = lo - s.k * Hkv;
+        s.b = blocks[s.k];
+        s.i = (int)div64((int64_t)s.b.nt * (w - first_run[lo]), first_run[lo + 1] - first_run[lo]);
+      }
+      sp.runs[w] = s;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
 // runs and pieces
 // ---------------------------------------------------------------------------
 
-// A run's piece of a unit: tiles [i0, i1) of block b, KV head g (tile i is
-// cell tile kt_last - i).
+// A run's piece of a unit: tiles [i0, i1) of a block, KV head g (tile i is
+// cell tile kt0 + nt - 1 - i).
 struct Piece {
   SharedBlock b;
   int g;
@@ -300,30 +425,24 @@ struct Piece {
   __device__ __forceinline__ int kt(int i) const { return b.kt0 + b.nt - 1 - i; }
 };
 
-// Tiles of a unit at offset `at` of the work space, w work each, that a run
-// [t0, t1) holds: those whose first unit of work lies in it.
-__device__ __forceinline__ void run_tiles(int64_t at, int nt, int w, int64_t t0, int64_t t1, int* i0, int* i1) {
-  const int64_t a = t0 > at ? (t0 - at + w - 1) / w : 0, b = t1 > at ? (t1 - at + w - 1) / w : 0;
-  *i0 = (int)(a < nt ? a : nt);
-  *i1 = (int)(b < nt ? b : nt);
-}
-
 struct PieceCursor {
   const SharedBlock* blocks;
-  const int64_t* off;
-  int n_blk, Hkv, k, g, loaded;
-  int64_t t0, t1;
+  SharedBlock b;            // block k, once loaded
+  int k, g, i, loaded;
+  int ke, ge, ie;           // where the run ends
+  int Hkv;
   // The next piece with a tile (every role steps alike).
   __device__ __forceinline__ bool next(Piece* pc) {
-    while (k < n_blk) {
+    while (k < ke || (k == ke && (g < ge || (g == ge && i < ie)))) {
       if (loaded != k) {
-        pc->b = blocks[k];
+        b = blocks[k];
         loaded = k;
       }
-      const int64_t at = Hkv * off[k] + (int64_t)g * pc->b.nt * pc->b.w;
-      if (at >= t1) return false;
+      pc->b = b;
       pc->g = g;
-      run_tiles(at, pc->b.nt, pc->b.w, t0, t1, &pc->i0, &pc->i1);
+      pc->i0 = i;
+      pc->i1 = (k == ke && g == ge) ? ie : b.nt;
+      i = 0;
       if (++g == Hkv) {
         g = 0;
         ++k;
@@ -334,34 +453,18 @@ struct PieceCursor {
   }
 };
 
-// The cursor at the start of run `run` (called by whole warps: 32-ary search
-// for the last block whose work starts at or before the run).
-__device__ __forceinline__ PieceCursor run_cursor(const SharedPlan& sp, int run, int lane) {
+__device__ __forceinline__ PieceCursor run_cursor(const SharedPlan& sp, int run) {
   PieceCursor c;
+  const SharedRun* s = sp.runs + run;
   c.blocks = sp.blocks;
-  c.off = sp.blk_off;
-  c.n_blk = *sp.n_blk;
+  c.k = c.loaded = s->k;
+  c.g = s->g;
+  c.i = s->i;
+  c.b = s->b;
+  c.ke = s[1].k;
+  c.ge = s[1].g;
+  c.ie = s[1].i;
   c.Hkv = sp.p.d.Hkv;
-  c.loaded = -1;
-  c.k = c.g = 0;
-  const int64_t T = c.n_blk > 0 ? c.Hkv * c.off[c.n_blk] : 0;
-  c.t0 = T * run / sp.W;
-  c.t1 = T * (run + 1) / sp.W;
-  if (c.t0 >= c.t1) {
-    c.n_blk = 0;
-    return c;
-  }
-  int lo = 0, hi = c.n_blk;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int probe = lo + lane * step;
-    const unsigned m = __ballot_sync(0xffffffffu, probe < hi && c.Hkv * c.off[probe] <= c.t0);
-    const int q = 31 - __clz(m);   // lane 0 always qualifies
-    lo += q * step;
-    hi = min(hi, lo + step);
-  }
-  c.k = lo;
-  c.g = (int)((c.t0 - c.Hkv * c.off[lo]) / (c.off[lo + 1] - c.off[lo]));
   return c;
 }
 
@@ -493,6 +596,12 @@ __device__ __noinline__ void sh_pv_cuda_cores(uint32_t tP, int a, int b, const u
     tmem_st32(tO + ch * 32, ou);
     tmem_wait_st();
   }
+}
+
+// 8 floats to a 32-byte aligned address: a whole sector per lane.
+__device__ __forceinline__ void st_global_v8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
 }
 
 // 32 consecutive output values starting at element i0.
@@ -729,9 +838,9 @@ __device__ __forceinline__ void sh_softmax(const SharedPlan& sp, PieceCursor cur
         if (fin) {
           sh_store32(sp.p.d.out, ob + ch * 32, v, sp.out_vec != 0);
         } else {
-          float4* dst = reinterpret_cast<float4*>(sp.rec_o + rec * D + ch * 32);
+          float* dst = sp.rec_o + rec * D + ch * 32;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          for (int q = 0; q < 32; q += 8) st_global_v8(dst + q, v + q);
         }
       }
     }
@@ -816,7 +925,7 @@ shared_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   pdl_launch_dependents();
   pdl_wait_prior_grid();   // the plan
 
-  PieceCursor cur = run_cursor(sp, run, lane);
+  PieceCursor cur = run_cursor(sp, run);
 
   if (warp >= 4) {
     // ---- softmax warpgroups ----
@@ -996,85 +1105,6 @@ shared_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   }
 }
 
-// ---------------------------------------------------------------------------
-// combine
-// ---------------------------------------------------------------------------
-
-// The run that holds unit t of a work space of T units cut into W runs.
-__device__ __forceinline__ int64_t run_of(int64_t t, int64_t T, int64_t W) { return ((t + 1) * W + T - 1) / T - 1; }
-
-// One warp per (row, query head): records in order (the shared part's home
-// record and the records of the runs after it, then the own part's home
-// record and the slots of the warps after it), one online pass, then the sink.
-template <int D>
-__global__ void __launch_bounds__(128) shared_combine_kernel(const SharedPlan sp, const PagedPlan own) {
-  constexpr int EPL = D / 32;
-  pdl_launch_dependents();
-  pdl_wait_prior_grid();
-  const int64_t wid = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const DecodePlan& d = sp.p.d;
-  if (wid >= (int64_t)d.R * d.Hq) return;
-  const int r = (int)(wid / d.Hq), h = (int)(wid % d.Hq);
-  const int g = h / d.G, hh = h % d.G;
-
-  float M = neg_inf(), L = 0.f, O[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) O[i] = 0.f;
-  auto fold = [&](const float* o, const float* ml) {
-    const float2 x = *reinterpret_cast<const float2*>(ml);
-    const float mn = fmax_nan(M, x.x), mu = (mn == neg_inf()) ? 0.f : mn;
-    const float c = ex2((M - mu) * kLog2e), f = ex2((x.x - mu) * kLog2e);
-    L = fmaf(L, c, x.y * f);
-#pragma unroll
-    for (int i = 0; i < EPL; i += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(o + lane * EPL + i);
-      O[i] = fmaf(O[i], c, v.x * f);
-      O[i + 1] = fmaf(O[i + 1], c, v.y * f);
-    }
-    M = mn;
-  };
-
-  const int64_t nt_own = own.d.row_tiles[r + 1] - own.d.row_tiles[r];
-  const int k = sp.row_blk[r];
-  if (k >= 0) {
-    const SharedBlock b = sp.blocks[k];
-    if (b.nt > 0) {
-      const int64_t T = d.Hkv * sp.blk_off[*sp.n_blk], W = sp.W;
-      const int64_t at = d.Hkv * sp.blk_off[k] + (int64_t)g * b.nt * b.w;
-      const int64_t w0 = run_of(at, T, W), w1 = run_of(at + (int64_t)(b.nt - 1) * b.w, T, W);
-      const int j = r - b.row0, slot = (b.w == 2 && j >= sp.rpt) ? 1 : 0;
-      const int64_t lane_rec = slot * 128 + (j - slot * sp.rpt) * d.G + hh;
-      if (w0 == w1 && nt_own == 0) return;   // finished by its only piece
-      int64_t rec = (int64_t)r * d.Hq + h;
-      fold(sp.rec_o + rec * D, sp.rec_ml + rec * 2);
-      for (int64_t w = w0 + 1; w <= w1; ++w) {
-        int i0, i1;
-        run_tiles(at, b.nt, b.w, T * w / W, T * (w + 1) / W, &i0, &i1);
-        if (i0 >= i1) continue;
-        rec = (int64_t)d.R * d.Hq + w * 256 + lane_rec;
-        fold(sp.rec_o + rec * D, sp.rec_ml + rec * 2);
-      }
-    }
-  }
-  if (nt_own > 0) {
-    const int64_t T = (int64_t)d.Hkv * own.d.row_tiles[d.R], W = own.d.W;
-    const int64_t at = (int64_t)d.Hkv * own.d.row_tiles[r] + g * nt_own;
-    const int64_t w0 = run_of(at, T, W), w1 = run_of(at + nt_own - 1, T, W);
-    int64_t rec = (W + (int64_t)r * d.Hkv + g) * d.G + hh;
-    fold(own.d.part.o + rec * D, own.d.part.ml + rec * 2);
-    for (int64_t w = w0 + 1; w <= w1; ++w) {
-      if (T * w / W >= T * (w + 1) / W) continue;   // (fewer tiles than warps: an empty run)
-      rec = w * d.G + hh;
-      fold(own.d.part.o + rec * D, own.d.part.ml + rec * 2);
-    }
-  }
-  const float sigma = d.lg.sinks ? __ldg(d.lg.sinks + h) : neg_inf();
-  const int64_t ob = (int64_t)r * d.out.sr + (int64_t)h * d.out.sh + lane * EPL;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) store_from_float(d.out.out, ob + i, d.out.type, fold_with_sink(M, L, O[i], sigma));
-}
-
 template <typename KT, int D, bool PLAIN>
 cudaError_t launch_sh_t(const SharedPlan& sp, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                         cudaStream_t stream) {
@@ -1090,8 +1120,11 @@ cudaError_t launch_sh_t(const SharedPlan& sp, const CUtensorMap& tmQ, const CUte
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  static std::atomic<unsigned long long> plan_set{0ull};
+  if ((e = set_smem_limit_once(plan_set, shared_plan_kernel, (int)sizeof(PlanShared))) != cudaSuccess) return e;
   cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(1024);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = sp.max_blk <= kPlanBlocks ? sizeof(PlanShared) : 32 * sizeof(long long);
   if ((e = cudaLaunchKernelEx(&cfg, shared_plan_kernel, sp)) != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)sp.W);
   cfg.blockDim = dim3(L::THREADS);
@@ -1118,24 +1151,6 @@ cudaError_t launch_shared(const SharedPlan& sp, const CUtensorMap& tmQ, const CU
                         : launch_sh_d<__half, 128>(sp, tmQ, tmK, tmV, stream);
     default: return bf ? launch_sh_d<__nv_bfloat16, 256>(sp, tmQ, tmK, tmV, stream)
                        : launch_sh_d<__half, 256>(sp, tmQ, tmK, tmV, stream);
-  }
-}
-
-cudaError_t launch_shared_combine(const SharedPlan& sp, const PagedPlan& own, cudaStream_t stream) {
-  const int64_t blocks = ((int64_t)sp.p.d.R * sp.p.d.Hq + 3) / 4;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  switch (sp.p.d.D) {
-    case 64: return cudaLaunchKernelEx(&cfg, shared_combine_kernel<64>, sp, own);
-    case 128: return cudaLaunchKernelEx(&cfg, shared_combine_kernel<128>, sp, own);
-    default: return cudaLaunchKernelEx(&cfg, shared_combine_kernel<256>, sp, own);
   }
 }
 

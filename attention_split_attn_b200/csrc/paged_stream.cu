@@ -158,7 +158,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   const int64_t W = p.d.W, Hkv = p.d.Hkv;
   const int64_t T = Hkv * row_tiles[p.d.R];
   const int64_t w = blockIdx.x;
-  const int64_t t0 = T * w / W, t1 = T * (w + 1) / W;
+  const int64_t t0 = div64(T * w, W), t1 = div64(T * (w + 1), W);
   if (t0 >= t1) return;
 
   // the row holding tile t0: the last r with Hkv * row_tiles[r] <= t0
@@ -179,8 +179,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   ps_load_row(p, row_tiles, c);
   {
     const int64_t off = t0 - Hkv * row_tiles[c.r];
-    c.g = (int)(off / c.nt);
-    c.j = off % c.nt;
+    c.g = (int)div64(off, c.nt);
+    c.j = off - c.g * c.nt;
   }
   PsCursor ic = c;   // issue cursor, NS tiles ahead (the same in every lane)
   const int64_t n = t1 - t0;

@@ -414,8 +414,9 @@ int32_t attn_append_paged(const attn_append_args *args, void *stream);
  * read once for the group, through the table of its first row, whatever pages
  * the other rows name there.  Rows of no group run as in attn_decode_paged.
  * A group_begin that decreases or passes n_rows records ATTN_ERR_INVALID_ARG
- * and no row is grouped.  Over an e4m3 / int8 cache every row reads its own
- * table (the same result, nothing shared).                                 */
+ * and no row is grouped.  Over an e4m3 / int8 cache, or where the tables of
+ * all rows together hold less than 64 MB of K and V, every row reads its own
+ * table (the same result, nothing shared, the groups are not looked at).   */
 typedef struct {
     int32_t n_rows, n_head_q, n_head_kv, head_dim;
     int32_t n_pages, page_size;              /* n_pages * page_size < 2^31      */

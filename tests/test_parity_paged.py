@@ -305,10 +305,16 @@ class Case:
         return ref.attention(self.q, self.k, self.v, self.table, self.ends, row_begin=self.begins,
                              row_table=self.row_table, slopes=self.slopes, sinks=self.sinks, **self.kw, **self.scales)
 
-    def args(self, op):
+    def args(self, op, narrow=False):
+        # decode_shared runs row by row where the tables cannot hold much: tables wide enough that it does not (the
+        # entries behind a row's pages are never read), unless narrow
+        cell = len(self.ends) * self.k.shape[2] * self.k.shape[3] * 4
+        cols = self.table.shape[1] if narrow or op != A.OP_DECODE_SHARED else (65 << 20) // (cell * self.k.shape[1]) + 1
+        table = torch.full((self.table.shape[0], max(cols, self.table.shape[1])), -7, dtype=I32)
+        table[:, :self.table.shape[1]] = self.table
         up = lambda t: None if t is None else t.cuda()
         like = lambda t: torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device="cuda").copy_(t)
-        self.dev = dict(q=up(self.q), k=like(self.k), v=like(self.v), table=up(self.table), ends=up(self.ends),
+        self.dev = dict(q=up(self.q), k=like(self.k), v=like(self.v), table=up(table), ends=up(self.ends),
                         out=torch.full(self.q.shape, math.nan, dtype=self.out_dtype, device="cuda"))
         self.opt = dict(row_begin=up(self.begins), row_table=up(self.row_table), alibi_slopes=up(self.slopes),
                         sinks=up(self.sinks), **{n: up(t) for n, t in self.scales.items()})
@@ -317,8 +323,8 @@ class Case:
         d = self.dev
         return A.make_paged_args(d["q"], d["k"], d["v"], d["out"], d["table"], d["ends"], **self.kw, **self.opt)
 
-    def run(self, op):
-        a = self.args(op)
+    def run(self, op, narrow=False):
+        a = self.args(op, narrow)
         ws = poisoned_workspace(A.paged_workspace_size(a, op))
         fn = A.attn_decode_paged_args if op == A.OP_DECODE_PAGED else A.attn_decode_shared_args
         fn(a, ws=ws)
@@ -326,8 +332,8 @@ class Case:
         return self.dev["out"]
 
 
-def check(case, op=A.OP_DECODE_PAGED, want=None):
-    got = case.run(op)
+def check(case, op=A.OP_DECODE_PAGED, want=None, narrow=False):
+    got = case.run(op, narrow)
     A.check_device_status()
     want = case.expected() if want is None else want
     compare(got, want, 1e-5, 2e-2)
@@ -548,6 +554,21 @@ def test_shared_groups_that_cannot_be(cuda_lib, begin):
 @pytest.mark.parametrize("cache", ["e4m3", "i8"])
 def test_shared_one_byte(cuda_lib, cache):
     check(Case(28, [300, 301, 450, 299], D=128, P=16, cache=cache, groups=[(4, 299)]), A.OP_DECODE_SHARED)
+
+
+def test_shared_over_narrow_tables(cuda_lib):
+    """Tables that hold little are read row by row: the same result, and group arrays that cannot be do not matter."""
+    c = Case(34, [300, 301, 450, 299], D=64, P=16, groups=[(4, 299)], sinks=True)
+    check(c, A.OP_DECODE_SHARED, narrow=True)
+
+
+def test_shared_many_blocks(cuda_lib):
+    """More blocks than the planner keeps in shared memory, and more units than runs."""
+    n = 2500
+    rng = np.random.default_rng(35)
+    table_of = (np.arange(n) // 2).tolist()
+    ends = (20 + rng.integers(0, 30, n)).tolist()
+    check(Case(35, ends, D=64, P=16, Hq=2, Hkv=1, row_table=table_of, groups=[(2, 25)] * (n // 2)), A.OP_DECODE_SHARED)
 
 
 def test_shared_is_deterministic(cuda_lib):
