@@ -138,7 +138,20 @@ __device__ __forceinline__ bool sh_wait_warp(uint64_t* bar, uint32_t parity, int
   return __all_sync(0xffffffffu, ok);
 }
 
-// The i-th use of an N-stage ring: its stage and its barriers' phase.
+// A place in an N-stage ring and its barriers' phase (the MMA issuer's: no
+// division between a barrier and the MMAs behind it).
+template <int N>
+struct RingPos {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == N) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+// The i-th use of an N-stage ring.
 template <int N>
 __device__ __forceinline__ int ring_stage(int64_t i) { return (int)(i % N); }
 template <int N>
@@ -1003,39 +1016,42 @@ shared_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         const uint64_t k_desc = umma_desc_sw128(smem_u32(sm + L::OFF_K), 16, 1024);
         const uint64_t v_desc = umma_desc_sw128(smem_u32(sm + L::OFF_V), L::BOX, 1024);
         constexpr uint64_t kTileDesc = (uint64_t)(L::TILE >> 4);
-        int64_t ck = 0, cv = 0, nQ = 0;
-        uint32_t n_p[2] = {0, 0};
+        RingPos<NK> ck;
+        RingPos<NV> cv;
+        int64_t nQ = 0;
+        uint32_t n_p0 = 0, n_p1 = 0;
         bool ok = true;
         Piece pc;
         // S of the next K tile for slots [s0, s1) (Q tile = slot, or 0 for a
         // block of one tile of rows), then that K stage is free
         auto wait_k = [&]() {
-          if (!sh_wait(&B.k_full[ring_stage<NK>(ck)], ring_phase<NK>(ck), status, abort_flag)) return false;
+          if (!sh_wait(&B.k_full[ck.stage], ck.phase, status, abort_flag)) return false;
           tc_fence_after();
           return true;
         };
         auto issue_s = [&](int s, int q) {
           sh_issue_s<D>(tmem + (uint32_t)s * 128u, q_desc + (uint64_t)q * kTileDesc,
-                        k_desc + (uint64_t)ring_stage<NK>(ck) * kTileDesc, idS);
+                        k_desc + (uint64_t)ck.stage * kTileDesc, idS);
           umma_commit(&B.s_full[s]);
         };
         auto k_done = [&]() {
-          umma_commit(&B.k_empty[ring_stage<NK>(ck)]);
-          ++ck;
+          umma_commit(&B.k_empty[ck.stage]);
+          ck.next();
         };
         auto wait_p = [&](int s) {
-          const bool w = sh_wait(&B.p_full[s], n_p[s] & 1u, status, abort_flag);
-          ++n_p[s];
+          const bool w = sh_wait(&B.p_full[s], (s ? n_p1 : n_p0) & 1u, status, abort_flag);
+          if (s) ++n_p1;
+          else ++n_p0;
           tc_fence_after();
           return w;
         };
         auto issue_pv = [&](int s, bool acc) {
           if (bad_flag[s] == 0)
             sh_issue_pv<D>(tmem + 256u + (uint32_t)s * D, tmem + (uint32_t)s * 128u,
-                           v_desc + (uint64_t)ring_stage<NV>(cv) * kTileDesc, idO, acc);
+                           v_desc + (uint64_t)cv.stage * kTileDesc, idO, acc);
         };
         auto wait_v = [&]() {
-          const bool w = sh_wait(&B.v_full[ring_stage<NV>(cv)], ring_phase<NV>(cv), status, abort_flag);
+          const bool w = sh_wait(&B.v_full[cv.stage], cv.phase, status, abort_flag);
           tc_fence_after();
           return w;
         };
@@ -1053,7 +1069,7 @@ shared_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
               const bool more = i + 1 < n;
               if (!more) umma_commit(B.q_empty);   // every S of the piece is issued
               for (int s = 0; s < slots; ++s) {
-                if (!wait_p(s) || (s == 0 && !wait_v())) { ok = false; break; }
+                if ((s == 0 && !wait_v()) || !wait_p(s)) { ok = false; break; }
                 issue_pv(s, i > 0);
                 if (!more) {
                   umma_commit(&B.pv_done[s]);
@@ -1064,8 +1080,8 @@ shared_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 }
               }
               if (!ok) break;
-              umma_commit(&B.v_empty[ring_stage<NV>(cv)]);
-              ++cv;
+              umma_commit(&B.v_empty[cv.stage]);
+              cv.next();
             }
           } else {
             for (int i = 0; ok && i < min(n, 2); ++i) {
@@ -1076,10 +1092,10 @@ shared_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             if (ok && n <= 2) umma_commit(B.q_empty);
             for (int i = 0; ok && i < n; ++i) {
               const int s = i & 1;
-              if (!wait_p(s) || !wait_v()) { ok = false; break; }
+              if (!wait_v() || !wait_p(s)) { ok = false; break; }
               issue_pv(s, i >= 2);
-              umma_commit(&B.v_empty[ring_stage<NV>(cv)]);
-              ++cv;
+              umma_commit(&B.v_empty[cv.stage]);
+              cv.next();
               if (i + 2 < n) {
                 if (!wait_k()) { ok = false; break; }
                 issue_s(s, 0);
