@@ -139,6 +139,8 @@ _lib = None
 def load_library():
     """Load libattn_b200.so; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -510,6 +512,10 @@ class PageTables(NamedTuple):
     free_state: torch.Tensor   # [2] ring state after the step
 
 
+# The current stream's handle without building a torch.cuda.Stream (0.2 against 1.2 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _on_device(a, *tensors):
     """All tensors on one CUDA device, kept with the argument block for the calls."""
     devs = {t.device for t in tensors if t is not None}
@@ -524,7 +530,7 @@ def _stream_on(a, stream) -> int:
     cur = torch.cuda.current_device()
     if a.device != cur:
         raise ValueError(f"tensors are on cuda:{a.device}, the current device is cuda:{cur}")
-    return _stream_handle(stream)
+    return _raw_stream(cur) if stream is None else stream.cuda_stream
 
 
 def _check_pool(k, v):

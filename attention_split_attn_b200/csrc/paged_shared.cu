@@ -163,7 +163,7 @@ __device__ __forceinline__ uint32_t ring_phase(int64_t i) { return (uint32_t)((i
 
 // One CTA: everything between its loads and its stores happens in shared
 // memory, so its time is a few dependent loads and barriers.
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;   // at most; 256 for few rows and groups (cheaper barriers)
 constexpr int kPlanBlocks = 1024;   // blocks kept in shared memory; a plan that may hold more works in the workspace
 
 // Exclusive scan of x over the CTA on top of *carry (the same in every
@@ -179,7 +179,7 @@ __device__ __forceinline__ int64_t cta_excl_scan(int64_t x, int64_t* carry, long
   __syncthreads();   // the previous scan's sums are read
   if (lane == 31) wsum[wid] = v;
   __syncthreads();
-  int64_t s = wsum[lane];
+  int64_t s = lane < (int)(blockDim.x >> 5) ? wsum[lane] : 0;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, s, off);
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   pdl_launch_dependents();
   pdl_wait_prior_grid();
   const PagedPlan& p = sp.p;
-  const int tid = threadIdx.x, R = p.d.R, Hkv = p.d.Hkv;
+  const int tid = threadIdx.x, nthr = blockDim.x, R = p.d.R, Hkv = p.d.Hkv;
   const bool in_smem = sp.max_blk <= kPlanBlocks;
   PlanShared* ps = reinterpret_cast<PlanShared*>(plan_smem);
   SharedBlock* blocks = in_smem ? ps->blocks : sp.blocks;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
 
   // 1. are the groups well formed?
   bool bad = false;
-  for (int i = tid; i <= sp.n_groups; i += kPlanThreads) {
+  for (int i = tid; i <= sp.n_groups; i += nthr) {
     const int b = __ldg(sp.group_begin + i);
     bad |= b < 0 || b > R || (i > 0 && b < __ldg(sp.group_begin + i - 1));
   }
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   // 2. blocks of at most block_rows rows (a group of one row shares nothing)
   const int cap = p.width * p.P;
   int64_t nb = 0;
-  for (int base = 0; base < n_groups; base += kPlanThreads) {
+  for (int base = 0; base < n_groups; base += nthr) {
     const int i = base + tid;
     int r0 = 0, n = 0, len = 0, table = 0;
     if (i < n_groups) {
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
 
   // 3. rows: their block, its cell range, and the own parts' tile prefix
   int64_t carry = 0;
-  for (int base = 0; base < R; base += kPlanThreads) {
+  for (int base = 0; base < R; base += nthr) {
     const int r = base + tid;
     int64_t tiles = 0;
     if (r < R) {
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
 
   // 4. the blocks' tiles, and the prefix of their work in tiles of one slot
   int64_t work = 0;
-  for (int base = 0; base < n_blk; base += kPlanThreads) {
+  for (int base = 0; base < n_blk; base += nthr) {
     const int k = base + tid;
     int64_t x = 0;
     if (k < n_blk) {
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   const bool parts = in_smem && (int64_t)n_blk * Hkv <= W && T > 0 && T <= 16 * W;
   const SharedRun none{n_blk, 0, 0, 0, {}};
   if (!parts) {
-    for (int w = tid; w <= W; w += kPlanThreads) {
+    for (int w = tid; w <= W; w += nthr) {
       SharedRun s = none;
       const int64_t t = div64(T * w, W);
       if (t < T) {
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
       }
       sp.runs[w] = s;
     }
-    for (int64_t base = 0; base < (int64_t)n_blk * Hkv; base += kPlanThreads) {
+    for (int64_t base = 0; base < (int64_t)n_blk * Hkv; base += nthr) {
       const int64_t u = base + tid;
       int2 v = make_int2(0, -1);
       if (u < (int64_t)n_blk * Hkv) {
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     const int units = n_blk * Hkv;
     int64_t used = 0;
     int* first_run = ps->first_run;
-    for (int base = 0; base < units; base += kPlanThreads) {
+    for (int base = 0; base < units; base += nthr) {
       const int u = base + tid;
       int n = 0;
       if (u < units) {
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     }
     if (tid == 0) first_run[units] = (int)used;
     __syncthreads();
-    for (int w = tid; w <= W; w += kPlanThreads) {
+    for (int w = tid; w <= W; w += nthr) {
       SharedRun s = none;
       if (w < used) {
         int lo = 0, hi = units;   // the last unit whose first run is at or before w
@@ -1068,13 +1068,13 @@ shared_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             for (int i = 0; ok && i < n; ++i) {
               const bool more = i + 1 < n;
               if (!more) umma_commit(B.q_empty);   // every S of the piece is issued
+              if (more && !wait_k()) { ok = false; break; }
               for (int s = 0; s < slots; ++s) {
                 if ((s == 0 && !wait_v()) || !wait_p(s)) { ok = false; break; }
                 issue_pv(s, i > 0);
                 if (!more) {
                   umma_commit(&B.pv_done[s]);
                 } else {
-                  if (s == 0 && !wait_k()) { ok = false; break; }
                   issue_s(s, s);
                   if (s == slots - 1) k_done();
                 }
@@ -1139,7 +1139,7 @@ cudaError_t launch_sh_t(const SharedPlan& sp, const CUtensorMap& tmQ, const CUte
   static std::atomic<unsigned long long> plan_set{0ull};
   if ((e = set_smem_limit_once(plan_set, shared_plan_kernel, (int)sizeof(PlanShared))) != cudaSuccess) return e;
   cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kPlanThreads);
+  cfg.blockDim = dim3(sp.p.d.R <= 256 && sp.n_groups < 256 ? 256 : kPlanThreads);
   cfg.dynamicSmemBytes = sp.max_blk <= kPlanBlocks ? sizeof(PlanShared) : 32 * sizeof(long long);
   if ((e = cudaLaunchKernelEx(&cfg, shared_plan_kernel, sp)) != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)sp.W);
