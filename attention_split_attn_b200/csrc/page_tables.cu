@@ -30,8 +30,7 @@ namespace {
 constexpr int kPtThreads = 512;
 constexpr int kPtMaxSeqs = 16384;
 
-// Inclusive scan of three 32-bit-safe sums over the CTA; returns the
-// exclusive values and adds the totals to carry.
+// Totals of the rounds so far: rows, pages asked for, pages returned.
 struct Sums {
   int64_t rows, need, rel;
 };
@@ -48,8 +47,8 @@ __device__ __forceinline__ int64_t warp_incl(int64_t x, int lane) {
 __device__ __forceinline__ int32_t sat32(int64_t x) { return (int32_t)(x > 0x7fffffffLL ? 0x7fffffffLL : x); }
 
 __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const PageTablesPlan p) {
-  // [n] end of the sequence's rows, and its first ring entry (>= 0: it grows;
-  // -1: it does not)
+  // [n] each: the end of the sequence's rows, its first ring entry (-1: it does
+  // not grow), and the first returned page of those that end
   extern __shared__ int32_t sh[];
   __shared__ int64_t wsum[3][kPtThreads / 32];
   __shared__ int32_t used_sh;
@@ -58,7 +57,8 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const PageTable
   int32_t* row_last = sh;
   int32_t* ring_first = sh + n;
   int32_t* rel_first = sh + 2 * n;
-  pdl_launch_dependents();
+  // No early trigger for the next kernel: it may look at row_end before its own
+  // wait (attn_decode's prefix of few rows does).
   pdl_wait_prior_grid();
   int32_t head = __ldg(a.free_state), count = __ldg(a.free_state + 1);
   if (head < 0 || head >= a.n_pages || count < 0 || count > a.n_pages) {

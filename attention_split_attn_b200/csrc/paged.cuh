@@ -24,8 +24,8 @@ __device__ __forceinline__ PagedRow paged_row(const PagedPlan& p, int r) {
   v.begin = max(b, 0);
   v.end = max(min(v.raw_end, p.width * p.P), v.begin);
   v.table = p.row_table ? __ldg(p.row_table + r) : r;
-  if (v.table < 0 || v.table >= p.n_tables) {
-    record_status(p.d.status, ATTN_ERR_INVALID_ARG);
+  if (v.table < 0 || v.table >= p.n_tables) {   // padding rows (an empty range) may name no table
+    if (v.end > v.begin) record_status(p.d.status, ATTN_ERR_INVALID_ARG);
     v.table = 0;
     v.end = v.begin;
   }

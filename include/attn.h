@@ -402,8 +402,9 @@ int32_t attn_append_paged(const attn_append_args *args, void *stream);
  * outside a row's range never reach it, whatever their pages hold.  Table
  * entries that no range reaches are not read.  An entry outside [0, n_pages)
  * inside a range reads as cells of zeros, a row_table entry outside
- * [0, n_tables) makes its row see nothing, and both record
- * ATTN_ERR_INVALID_ARG in the device status word.
+ * [0, n_tables) of a row with a range makes the row see nothing, and both
+ * record ATTN_ERR_INVALID_ARG in the device status word (padding rows, whose
+ * range is empty, may name no table: row_seq of attn_page_tables serves).
  * Types: a 16-bit cache with Q in its dtype, head_dim 64, 128 or 256, up to 16
  * query heads per KV head; or an e4m3 / int8 cache (scales indexed by slot)
  * with Q in F16 or BF16, head_dim 128 or 256, up to 8.  Any of F32, F16, BF16

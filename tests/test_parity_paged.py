@@ -83,6 +83,38 @@ def test_page_tables(cuda_lib, n, P):
     _check_tables(lens, new, table, ring, state, P, int(np.maximum(new, 0).sum()) + 7, keep)
 
 
+def test_page_tables_of_the_most_sequences(cuda_lib):
+    rng = np.random.default_rng(4)
+    n = 16384
+    lens, new = rng.integers(0, 40, n), rng.integers(-1, 3, n)
+    table, ring, state = _pool_state(rng, lens, 16, 4, spare=n)
+    _check_tables(lens, new, table, ring, state, 16, 2 * n)
+
+
+def test_page_tables_then_flat_decode(cuda_lib):
+    """attn_decode right behind attn_page_tables reads the row ends of that step, call after call."""
+    k = torch.randn(64, 2, 64, device="cuda").to(torch.bfloat16)
+    q = torch.randn(4, 4, 64, device="cuda").to(torch.bfloat16)
+    out = torch.empty_like(q)
+    new, table, ring = i32([1] * 4).cuda(), torch.zeros(4, 4, dtype=I32, device="cuda"), torch.arange(16).to(I32).cuda()
+    lens = [i32([a, 3, 17, 40 - a]).cuda() for a in range(30)]
+    pa = [A.make_page_args(x, new, table.clone(), ring.clone(), i32([0, 16]).cuda(), page_size=16, n_rows=4)
+          for x in lens]
+    da = [A.make_args(q, k, k, out, scale=0.1, row_begin=torch.zeros(4, dtype=I32, device="cuda"),
+                      row_end=a.outputs.row_end) for a in pa]
+    ws = torch.empty(A.workspace_size(da[0], A.OP_DECODE), dtype=torch.uint8, device="cuda")
+    outs = []
+    for a, d in zip(pa, da):
+        A.attn_page_tables_args(a)
+        A.attn_decode_args(d, ws=ws)
+        outs.append(out.clone())
+    torch.cuda.synchronize()
+    pages = k.reshape(4, 16, 2, 64)
+    for x, got in zip(lens, outs):
+        compare(got, ref.attention(q.cpu(), pages.cpu(), pages.cpu(), i32([[0, 1, 2, 3]]), x.cpu() + 1, scale=0.1,
+                                   row_table=[0] * 4), 1e-5, 2e-2)
+
+
 @pytest.mark.parametrize("what", ["ring", "rows", "width"])
 def test_page_tables_sequences_that_cannot_grow(cuda_lib, what):
     rng = np.random.default_rng(5)
@@ -611,7 +643,7 @@ def _serve(graph, cache="bf16"):
     def step():
         A.attn_page_tables_args(pa)
         A.attn_append_paged_args(aa)
-        row_table.copy_(o.row_seq.clamp(min=0))
+        row_table.copy_(o.row_seq)
         A.attn_decode_shared_args(sa, ws=ws)
         out2.copy_(out)
         A.attn_decode_paged_args(da, ws=ws)
