@@ -580,9 +580,14 @@ int32_t encode_map(CUtensorMap* map, const void* base, int32_t type, int rank, c
     one[i] = 1u;
     if (i + 1 < rank) st[i] = (cuuint64_t)strides_bytes[i];
   }
+  // 256-byte fetches into L2 only where a head's row has 256 bytes: over 128-byte
+  // rows (e4m3 at head dim 128) they read the next head's row too, which is gone
+  // again before its own turn (699 MB of DRAM reads for 529 MB of an e4m3 pool).
+  const CUtensorMapL2promotion prom = dims[0] * dtype_size(type) >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                                                        : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
   const CUresult r = enc(map, tma_dtype(type), (cuuint32_t)rank, const_cast<void*>(base), d, st, b, one,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, prom,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return ATTN_OK;
 }
