@@ -11,6 +11,8 @@
 // load latency once per 32 tiles and not per tile; the tile's TMA box is
 // {128 bytes, 1 head, 16 cells, 1 page} of a 4-D map over [page][cell][head][D].
 // An id outside the pool is replaced by n_pages, where the TMA reads zeros.
+// 16 rows of 1024 to 8192 cells (302 MB, 8 KV heads, D 128, bf16): 47.5 us, 6.4
+// TB/s; one row of 130857 cells (536 MB): 80 to 86 us.
 #include <algorithm>
 
 #include "common.cuh"
