@@ -12,6 +12,7 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -283,12 +284,26 @@ def supports(args: AttnArgs, op: int) -> int:
     return int(load_library().attn_supports(ctypes.byref(args), op))
 
 
-def _workspace(nbytes: int, device, ws: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+def _allocating_on(stream):
+    """Allocations for a call on `stream` come from that stream's pool: a block of the current stream's pool may still
+    be in use by work queued there, which `stream` does not wait for."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _workspace(nbytes: int, device, ws: Optional[torch.Tensor], stream) -> Optional[torch.Tensor]:
     if nbytes == 0:
         return ws
     if ws is not None and ws.numel() * ws.element_size() >= nbytes and ws.data_ptr() % 256 == 0:
         return ws
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with _allocating_on(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _used_here_too(stream, *tensors):
+    """Results allocated for a call on `stream` are the caller's, who reads them on the current one."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream())
 
 
 def _stream_handle(stream) -> int:
@@ -301,7 +316,7 @@ def attn_decode_args(args: AttnArgs, ws: Optional[torch.Tensor] = None, stream=N
     lib = load_library()
     need = workspace_size(args, OP_DECODE)
     dev = torch.device("cuda", torch.cuda.current_device())
-    ws = _workspace(need, dev, ws)
+    ws = _workspace(need, dev, ws, stream)
     st = lib.attn_decode(ctypes.byref(args), None if ws is None else ws.data_ptr(),
                          0 if ws is None else ws.numel() * ws.element_size(), _stream_handle(stream))
     _raise_if(st, "attn_decode")
@@ -321,7 +336,7 @@ def attn_decode_append_args(args: AttnArgs, k_new: torch.Tensor, v_new: torch.Te
     lib = load_library()
     need = workspace_size(args, OP_DECODE)
     dev = torch.device("cuda", torch.cuda.current_device())
-    ws = _workspace(need, dev, ws)
+    ws = _workspace(need, dev, ws, stream)
     st = lib.attn_decode_append(ctypes.byref(args), k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0),
                                 k_new.stride(1), None if ws is None else ws.data_ptr(),
                                 0 if ws is None else ws.numel() * ws.element_size(), _stream_handle(stream))
@@ -360,7 +375,7 @@ def attn_prefill_args(args: AttnArgs, ws: Optional[torch.Tensor] = None, stream=
     lib = load_library()
     need = workspace_size(args, OP_PREFILL)
     dev = torch.device("cuda", torch.cuda.current_device())
-    ws = _workspace(need, dev, ws)
+    ws = _workspace(need, dev, ws, stream)
     st = lib.attn_prefill(ctypes.byref(args), None if ws is None else ws.data_ptr(),
                           0 if ws is None else ws.numel() * ws.element_size(), _stream_handle(stream))
     _raise_if(st, "attn_prefill")
@@ -415,7 +430,7 @@ def attn_selected_args(args: AttnSelectedArgs, ws: Optional[torch.Tensor] = None
     _raise_if(lib.attn_supports(ctypes.byref(args.base), OP_SELECTED), "attn_supports")
     need = int(lib.attn_workspace_size(ctypes.byref(args.base), OP_SELECTED, args.n_sel))
     dev = torch.device("cuda", torch.cuda.current_device())
-    ws = _workspace(need, dev, ws)
+    ws = _workspace(need, dev, ws, stream)
     st = lib.attn_selected(ctypes.byref(args), None if ws is None else ws.data_ptr(),
                            0 if ws is None else ws.numel() * ws.element_size(), _stream_handle(stream))
     _raise_if(st, "attn_selected")
@@ -443,7 +458,7 @@ def attn_selected_masked_args(args: AttnSelectedArgs, ws: Optional[torch.Tensor]
     _raise_if(lib.attn_supports(ctypes.byref(args.base), OP_SELECTED_MASKED), "attn_supports")
     need = int(lib.attn_workspace_size(ctypes.byref(args.base), OP_SELECTED_MASKED, args.n_sel))
     dev = torch.device("cuda", torch.cuda.current_device())
-    ws = _workspace(need, dev, ws)
+    ws = _workspace(need, dev, ws, stream)
     st = lib.attn_selected_masked(ctypes.byref(args), None if ws is None else ws.data_ptr(),
                                   0 if ws is None else ws.numel() * ws.element_size(), _stream_handle(stream))
     _raise_if(st, "attn_selected_masked")
@@ -489,7 +504,9 @@ def tree_mask(parent: torch.Tensor, prefix_cells: int, n_cells: int, mask: Optio
     _check_i32("parent", parent, parent.numel())
     R = parent.numel()
     if mask is None:
-        mask = torch.empty((R, n_cells), dtype=torch.float32, device=parent.device)
+        with _allocating_on(stream):
+            mask = torch.empty((R, n_cells), dtype=torch.float32, device=parent.device)
+        _used_here_too(stream, mask)
     if mask.dtype != torch.float32 or mask.stride(1) != 1 or tuple(mask.shape) != (R, n_cells):
         raise ValueError("mask must be float32 [rows, n_cells] with contiguous cells")
     lib = load_library()
@@ -565,7 +582,8 @@ def make_page_args(seq_len, new_len, page_table, free_ring, free_state, *, page_
     """Fill an AttnPageArgs: seq_len, new_len [n_seqs], page_table [n_seqs,
     width] and free_ring [n_pages] are int32 CUDA tensors (the last two are
     updated by the call), free_state int32 [2].  outputs (a PageTables of int32
-    tensors) is allocated when not given and kept as `.outputs`."""
+    tensors) is allocated when not given, on the current stream (make the block
+    under the stream of its calls), and kept as `.outputs`."""
     n = seq_len.numel()
     for name, t, m in (("seq_len", seq_len, n), ("new_len", new_len, n), ("free_ring", free_ring, 0),
                        ("free_state", free_state, 2), ("n_keep", n_keep, n)):
@@ -599,7 +617,11 @@ def attn_page_tables_args(args: AttnPageArgs, stream=None) -> PageTables:
 def page_tables(seq_len, new_len, page_table, free_ring, free_state, *, stream=None, **kw) -> PageTables:
     """Grow and release the sequences' block tables for one step and write its
     slot map and row ranges (see include/attn.h)."""
-    return attn_page_tables_args(make_page_args(seq_len, new_len, page_table, free_ring, free_state, **kw), stream)
+    with _allocating_on(stream):
+        args = make_page_args(seq_len, new_len, page_table, free_ring, free_state, **kw)
+    if kw.get("outputs") is None:
+        _used_here_too(stream, *args.outputs)
+    return attn_page_tables_args(args, stream)
 
 
 def make_append_args(k_new, v_new, slot, k, v, *, k_scale=None, v_scale=None):
@@ -686,9 +708,7 @@ def paged_workspace_size(args: AttnPagedArgs, op: int) -> int:
 def _paged_call(fn, where, args, op, ws, stream):
     handle = _stream_on(args, stream)
     if ws is None:
-        ws = _workspace(paged_workspace_size(args, op), torch.device("cuda", args.device), None)
-        if ws is not None and stream is not None:
-            ws.record_stream(stream)   # allocated on the current stream, used on this one
+        ws = _workspace(paged_workspace_size(args, op), torch.device("cuda", args.device), None, stream)
     st = fn(ctypes.byref(args), None if ws is None else ws.data_ptr(),
             0 if ws is None else ws.numel() * ws.element_size(), handle)
     _raise_if(st, where)
