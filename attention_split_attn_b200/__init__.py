@@ -220,6 +220,12 @@ def _check_i32(name, t, n):
         raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of at least {n} entries")
 
 
+def _keep(a, *tensors):
+    """An argument block holds addresses: its tensors live as long as it does."""
+    a.tensors = tensors
+    return a
+
+
 def make_args(q, k, v, out, *, scale, softcap=0.0, row_begin=None, row_end=None, cell_seq=None,
               row_seq=None, cell_pos=None, row_pos=None, causal=False, mask=None, alibi_slopes=None,
               sinks=None, n_slices=0, max_row_len=0, grid_order=0, k_scale=None, v_scale=None):
@@ -265,7 +271,8 @@ def make_args(q, k, v, out, *, scale, softcap=0.0, row_begin=None, row_end=None,
         if k_scale.stride(0) != v_scale.stride(0):
             raise ValueError("k_scale and v_scale must share their cell stride")
         a.k_scale, a.v_scale, a.scale_stride_cell = k_scale.data_ptr(), v_scale.data_ptr(), k_scale.stride(0)
-    return a
+    return _keep(a, q, k, v, out, row_begin, row_end, cell_seq, row_seq, cell_pos, row_pos, mask, alibi_slopes, sinks,
+                 k_scale, v_scale)
 
 
 def _raise_if(status: int, where: str):
@@ -411,7 +418,8 @@ def make_selected_args(q, k, v, out, sel, *, sorted_out=None, count_out=None, **
     if kw.get("causal"):
         raise ValueError("selected-key attention is maskless (causal must be False)")
     a = AttnSelectedArgs()
-    a.base = make_args(q, k, v, out, **kw)
+    base = make_args(q, k, v, out, **kw)
+    a.base = base       # (a copy of the block, without the tensors it keeps)
     if sel.dtype != torch.int32 or not sel.is_cuda or sel.dim() != 2 or sel.stride(1) != 1:
         raise ValueError("sel must be an int32 CUDA tensor [rows, n_sel] with contiguous entries")
     a.sel, a.sel_stride_row, a.n_sel = sel.data_ptr(), sel.stride(0), sel.shape[1]
@@ -421,7 +429,7 @@ def make_selected_args(q, k, v, out, sel, *, sorted_out=None, count_out=None, **
             raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of shape {shape}")
     a.sel_sorted_out = _ptr(sorted_out)
     a.sel_count_out = _ptr(count_out)
-    return a
+    return _keep(a, sel, sorted_out, count_out, *base.tensors)
 
 
 def attn_selected_args(args: AttnSelectedArgs, ws: Optional[torch.Tensor] = None, stream=None):
@@ -534,12 +542,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.c
 
 
 def _on_device(a, *tensors):
-    """All tensors on one CUDA device, kept with the argument block for the calls."""
+    """All tensors on one CUDA device; the block keeps them for its calls."""
     devs = {t.device for t in tensors if t is not None}
     if len(devs) > 1 or any(d.type != "cuda" for d in devs):
         raise ValueError(f"tensors must be on one CUDA device, got {sorted(map(str, devs))}")
     a.device = next(iter(devs)).index
-    return a
+    return _keep(a, *tensors)
 
 
 def _stream_on(a, stream) -> int:
