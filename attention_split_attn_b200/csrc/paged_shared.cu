@@ -220,13 +220,26 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   PagedRow first_row{};
   if (tid < R) first_row = paged_row(p, tid);   // (own_lo of this plan is NULL: the whole range)
 
-  // 1. are the groups well formed?
-  bool bad = false;
+  // 1. are the groups well formed?  One that ends behind the rows is if its
+  // rows see nothing: a sequence whose rows did not fit (attn_page_tables'
+  // seq_row runs on, its rows have row_end 0).
+  bool any_bad = false, bad = false, past = false;
   for (int i = tid; i <= sp.n_groups; i += nthr) {
     const int b = __ldg(sp.group_begin + i);
-    bad |= b < 0 || b > R || (i > 0 && b < __ldg(sp.group_begin + i - 1));
+    bad |= b < 0 || (i == 0 && b > R) || (i > 0 && b < __ldg(sp.group_begin + i - 1));
+    past |= b > R;
   }
-  const bool any_bad = __syncthreads_or(bad);
+  if (__syncthreads_or(bad || past) && !(any_bad = __syncthreads_or(bad))) {
+    __shared__ int tail;   // the first row of the one group that ends behind the rows
+    for (int i = tid; i < sp.n_groups; i += nthr) {
+      const int b = __ldg(sp.group_begin + i);
+      if (b <= R && __ldg(sp.group_begin + i + 1) > R) tail = b;
+    }
+    __syncthreads();
+    bool seen = false;
+    for (int64_t r = (int64_t)tail + tid; r < R; r += nthr) seen |= paged_row(p, (int)r).tiles() > 0;
+    any_bad = __syncthreads_or(seen);
+  }
   if (any_bad && tid == 0) record_status(p.d.status, ATTN_ERR_INVALID_ARG);
   const int n_groups = any_bad ? 0 : sp.n_groups;
 
@@ -238,7 +251,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     int r0 = 0, n = 0, len = 0, table = 0;
     if (i < n_groups) {
       r0 = __ldg(sp.group_begin + i);
-      n = __ldg(sp.group_begin + i + 1) - r0;
+      n = min(__ldg(sp.group_begin + i + 1), R) - r0;   // (below 0 for a group behind the rows)
       len = min(__ldg(sp.group_len + i), cap);
       if (n > 0) table = p.row_table ? __ldg(p.row_table + r0) : r0;
       if (n < 2 || len <= 0 || table < 0 || table >= p.n_tables) n = 0;

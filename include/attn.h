@@ -338,12 +338,12 @@ enum { ATTN_OP_DECODE_PAGED = 4, ATTN_OP_DECODE_SHARED = 5 };
  *                 0; pages below it are shared with others) go to the tail of
  *                 the ring, and its length becomes 0.  Its table row stays.
  * The step's rows are numbered sequence after sequence (seq_row: where each
- * sequence's rows begin); row t gets its slot, its sequence and the number of
- * cells it may see, position + 1.  A sequence that cannot grow -- the ring is
- * empty, the table row is full, its rows pass n_rows -- is left as it was: its
- * length and table do not change, its rows get slot -1 and row_end 0, and
- * seq_len_out shows it.  Rows behind the last sequence get slot -1, row_seq -1
- * and row_end 0.
+ * sequence's rows begin, counted on past n_rows where they do not fit); row t
+ * gets its slot, its sequence and the number of cells it may see, position + 1.
+ * A sequence that cannot grow -- the ring is empty, the table row is full, its
+ * rows pass n_rows -- is left as it was: its length and table do not change,
+ * its rows get slot -1 and row_end 0, and seq_len_out shows it.  Rows behind
+ * the last sequence get slot -1, row_seq -1 and row_end 0.
  * Table entries and page ids are checked: a length outside [0, table_width *
  * page_size], an id outside [0, n_pages), a ring state that cannot be, or more
  * pages returned than the ring holds record ATTN_ERR_INVALID_ARG in the
@@ -414,10 +414,12 @@ int32_t attn_append_paged(const attn_append_args *args, void *stream);
  * i, and the first group_len[i] cells of their tables are the same; they are
  * read once for the group, through the table of its first row, whatever pages
  * the other rows name there.  Rows of no group run as in attn_decode_paged.
- * A group_begin that decreases or passes n_rows records ATTN_ERR_INVALID_ARG
- * and no row is grouped.  Over an e4m3 / int8 cache, or where the tables of
- * all rows together hold less than 64 MB of K and V, every row reads its own
- * table (the same result, nothing shared, the groups are not looked at).   */
+ * A group_begin that decreases, or that passes n_rows with rows of its group
+ * that see cells, records ATTN_ERR_INVALID_ARG and no row is grouped (seq_row
+ * of attn_page_tables serves, also when a sequence's rows did not fit).  Over
+ * an e4m3 / int8 cache, or where the tables of all rows together hold less
+ * than 64 MB of K and V, every row reads its own table (the same result,
+ * nothing shared, the groups are not looked at).                           */
 typedef struct {
     int32_t n_rows, n_head_q, n_head_kv, head_dim;
     int32_t n_pages, page_size;              /* n_pages * page_size < 2^31      */
