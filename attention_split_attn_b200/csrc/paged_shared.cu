@@ -539,10 +539,19 @@ __device__ __forceinline__ float sh_max128(const float* x) {
   return fmax_nan(fmax_nan(mx[0], mx[1]), fmax_nan(mx[2], mx[3]));
 }
 
-// c tanh(u / c), any u: tanh |y| = 1 - 2 / (e^(2|y|) + 1); NaN stays NaN.
-__device__ __forceinline__ float sh_cap_exact(float u, float c, float inv_c2) {
-  const float e = ex2(fabsf(u) * inv_c2);   // inv_c2 = 2 log2(e) / c
+// c tanh(u / c) of any u, y = u / c.  sh_cap_far: c (1 - 2 / (e^(2|y|) + 1)),
+// whose difference costs an error near 2e-7 c, whatever u.  sh_cap: the same
+// for |y| > 1/4, where that is 8e-7 of u at most, and below it the odd Taylor
+// series in y, u (1 + y^2 (-1/3 + ... + 62/2835 y^6)), off by 8.9e-3 y^10 <
+// 9e-9 of u before roundings.  NaN stays NaN.
+__device__ __forceinline__ float sh_cap_far(float u, float c, float k) {   // k = 2 log2(e) / c
+  const float e = ex2(fabsf(u) * k);
   return copysignf(c * (1.f - __fdividef(2.f, e + 1.f)), u);
+}
+__device__ __forceinline__ float sh_cap(float u, float c, float inv_c, float k) {
+  const float y = u * inv_c, w = y * y;
+  const float h = w * fmaf(w, fmaf(w, fmaf(w, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f);
+  return fabsf(y) <= 0.25f ? fmaf(u, h, u) : sh_cap_far(u, c, k);
 }
 
 // Logits of one lane's row of a tile in the log2 domain, with softcap and
@@ -550,7 +559,11 @@ __device__ __forceinline__ float sh_cap_exact(float u, float c, float inv_c2) {
 // row_end - 1 for every cell that counts.  The softcap is the odd Taylor
 // series of c tanh(u / c) through u^9 in the raw product s (coefficients with
 // scale and log2(e) folded in) where every |u| of the warp is at most 0.4 c --
-// truncation below 3.7e-7 c -- and exact elsewhere.
+// truncation below 3.7e-7 c.  Elsewhere, and where a coefficient would not be
+// a normal float (softcaps beyond about 2300 at head dim 128): sh_cap_far for c
+// <= 256, where its error is 6e-5 at most, an eighth of an f16 weight's rounding
+// step, and sh_cap beyond.  (Five groups at D 64 with c = 1, where every tile
+// goes there: 241 us, with sh_cap for all c 285 us.)
 __device__ __forceinline__ void sh_transform(const SharedPlan& sp, float* x, float ls, float off) {
   if (sp.p.d.lg.softcap > 0.f) {
     float sm = 0.f;
@@ -569,9 +582,15 @@ __device__ __forceinline__ void sh_transform(const SharedPlan& sp, float* x, flo
         x[i + 1] = y.y;
       }
     } else {
-      const float c = sp.p.d.lg.softcap, k = 2.f * kLog2e / c, scale = sp.p.d.lg.scale;
+      const float c = sp.p.d.lg.softcap, scale = sp.p.d.lg.scale;
+      const float inv_c = fminf(1.f / c, 3.0e38f), k = fminf(2.f * kLog2e / c, 3.0e38f);
+      if (c <= 256.f) {
 #pragma unroll
-      for (int i = 0; i < kShCells; ++i) x[i] = sh_cap_exact(x[i] * scale, c, k) * kLog2e;
+        for (int i = 0; i < kShCells; ++i) x[i] = sh_cap_far(x[i] * scale, c, k) * kLog2e;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kShCells; ++i) x[i] = sh_cap(x[i] * scale, c, inv_c, k) * kLog2e;
+      }
     }
   } else {
 #pragma unroll
