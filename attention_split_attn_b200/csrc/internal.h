@@ -303,6 +303,7 @@ struct SharedPlan {
   float s_lim, c3, c5, c7, c9;   // softcap series in the raw product (s_lim 0: not usable)
   int32_t plain;           // no softcap, no ALiBi, scale > 0
   int32_t out_vec;         // output rows may be written with 16-byte stores
+  uint64_t stall_ns;       // > 0: the softmax warps first wait that long on a barrier nothing arrives at
 };
 cudaError_t launch_shared(const SharedPlan& sp, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                           cudaStream_t stream);

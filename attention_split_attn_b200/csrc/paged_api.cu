@@ -134,13 +134,26 @@ int32_t check_append(const attn_append_args* a) {
   return ATTN_OK;
 }
 
+// Sharing takes four launches and a plan, about 10 us more than row by row,
+// and saves at most the reading of all rows' tables.  Below 64 MB of them (at
+// 5.4 TB/s 12 us) row by row is the faster form whatever the groups: 8 rows
+// of 1100 cells, 8 KV heads, D 128 (38 MB) take 16 us against 25 us.
+constexpr int64_t kShareBytes = 64LL << 20;
+bool runs_shared(const attn_paged_args* a, int32_t op) {
+  if (op != ATTN_OP_DECODE_SHARED || !is16(a->kv_type) || a->n_groups == 0 || a->n_pages == 0) return false;
+  const double bytes = (double)a->n_rows * a->n_head_kv * a->table_width * a->page_size * 4.0 * a->head_dim;
+  return bytes > (double)kShareBytes;
+}
+
 int32_t check_paged(const attn_paged_args* a, int32_t op_id) {
   const bool shared = op_id == ATTN_OP_DECODE_SHARED;
   if (op_id != ATTN_OP_DECODE_PAGED && !shared) return refuse(ATTN_ERR_INVALID_ARG, "unknown op %d", op_id);
   const char* op = shared ? "decode_shared" : "decode_paged";
   if (!a) return refuse(ATTN_ERR_INVALID_ARG, "args is NULL");
-  for (int i = 0; i < 4; ++i)
+  for (int i = 1; i < 4; ++i)
     if (a->reserved[i] != 0) return refuse(ATTN_ERR_INVALID_ARG, "reserved fields must be zero");
+  if (a->reserved[0] < 0 || a->reserved[0] > 1000000)
+    return refuse(ATTN_ERR_INVALID_ARG, "%s: reserved[0] (the bounded-wait test) must be 0..1000000 us", op);
   if (a->n_rows < 0 || a->n_tables < 0 || a->table_width < 0 || a->n_groups < 0)
     return refuse(ATTN_ERR_INVALID_ARG, "%s: negative size", op);
   if (a->n_head_q <= 0 || a->n_head_kv <= 0 || a->n_head_q % a->n_head_kv != 0)
@@ -193,6 +206,8 @@ int32_t check_paged(const attn_paged_args* a, int32_t op_id) {
     return refuse(ATTN_ERR_UNSUPPORTED, "%s: zero q stride", op);
   if ((int64_t)a->n_rows * a->n_head_q > 0x7fffffffLL)
     return refuse(ATTN_ERR_UNSUPPORTED, "%s: too many rows", op);
+  if (a->reserved[0] != 0 && !runs_shared(a, op_id))
+    return refuse(ATTN_ERR_INVALID_ARG, "%s: the bounded-wait test runs on the tensor-core kernel only", op);
   return ATTN_OK;
 }
 
@@ -220,16 +235,6 @@ struct SharedWs {
 int shared_slots(int D) { return D <= 128 ? 2 : 1; }
 int64_t shared_block_rows(const attn_paged_args* a) {
   return (int64_t)shared_slots(a->head_dim) * (128 / (a->n_head_q / a->n_head_kv));
-}
-// Sharing takes four launches and a plan, about 10 us more than row by row,
-// and saves at most the reading of all rows' tables.  Below 64 MB of them (at
-// 5.4 TB/s 12 us) row by row is the faster form whatever the groups: 8 rows
-// of 1100 cells, 8 KV heads, D 128 (38 MB) take 16 us against 25 us.
-constexpr int64_t kShareBytes = 64LL << 20;
-bool runs_shared(const attn_paged_args* a, int32_t op) {
-  if (op != ATTN_OP_DECODE_SHARED || !is16(a->kv_type) || a->n_groups == 0 || a->n_pages == 0) return false;
-  const double bytes = (double)a->n_rows * a->n_head_kv * a->table_width * a->page_size * 4.0 * a->head_dim;
-  return bytes > (double)kShareBytes;
 }
 size_t shared_max_blocks(const attn_paged_args* a) {
   return (size_t)std::min(a->n_groups, a->n_rows) + (size_t)a->n_rows / (size_t)shared_block_rows(a) + 1;
@@ -324,6 +329,7 @@ void fill_shared(SharedPlan* sp, const PagedPlan& p, const attn_paged_args* a, c
       sp->s_lim = (float)lim;
     }
   }
+  sp->stall_ns = (uint64_t)a->reserved[0] * 1000ull;
   const int64_t ovec = 16 / esize(a->out_type);
   sp->out_vec = aligned16(a->out) && (a->n_rows <= 1 || a->o_stride_row % ovec == 0) &&
                 (a->n_head_q <= 1 || a->o_stride_head % ovec == 0);

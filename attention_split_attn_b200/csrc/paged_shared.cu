@@ -53,7 +53,8 @@
 // slot's softmax (2050) and its P V and next S (2000) one after the other, the
 // two slots in turn, against 2048 cycles of tensor work.
 // All waits are bounded; a timeout records ATTN_ERR_DEVICE_TIMEOUT, raises a
-// CTA-wide flag that ends every role, drains the copies and frees TMEM.
+// CTA-wide flag that ends every role, drains the copies, makes every row of the
+// CTA's run NaN and frees TMEM.
 #include <algorithm>
 #include <cmath>
 
@@ -82,8 +83,8 @@ struct ShLayout {
   static constexpr int OFF_V = OFF_K + NK * TILE;
   static constexpr int OFF_BAR = OFF_V + NV * TILE;
   // q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV],
-  // s_full[2], p_full[2], pv_done[2], merge_full, merge_empty, mma_done
-  static constexpr int N_BAR = 2 + 2 * NK + 2 * NV + 6 + 3;
+  // s_full[2], p_full[2], pv_done[2], merge_full, merge_empty, mma_done, never
+  static constexpr int N_BAR = 2 + 2 * NK + 2 * NV + 6 + 4;
   static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;    // TMEM address, abort flag, first block, bad[2]
   static constexpr int OFF_ML = OFF_MISC + 32;            // [128][2] floats: slot 1's (m, l) at a merge
   static constexpr int BYTES = OFF_ML + kShRows * 8;
@@ -99,7 +100,7 @@ struct ShLayout {
 
 struct ShBars {
   uint64_t *q_full, *q_empty, *k_full, *k_empty, *v_full, *v_empty, *s_full, *p_full, *pv_done, *merge_full,
-      *merge_empty, *mma_done;
+      *merge_empty, *mma_done, *never;
 };
 
 template <int D>
@@ -119,17 +120,19 @@ __device__ __forceinline__ ShBars sh_bars(unsigned char* sm) {
   r.merge_full = r.pv_done + 2;
   r.merge_empty = r.merge_full + 1;
   r.mma_done = r.merge_empty + 1;
+  r.never = r.mma_done + 1;
   return r;
 }
 
-__device__ __forceinline__ bool sh_wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort_flag) {
+__device__ __forceinline__ bool sh_wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort_flag,
+                                        uint64_t limit_ns = kWaitLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t spin = 1;; ++spin) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((spin & 63u) == 0) {
       if (*abort_flag) return false;
-      if (global_timer_ns() - t0 > kWaitLimitNs) {
+      if (global_timer_ns() - t0 > limit_ns) {
         record_status(status, ATTN_ERR_DEVICE_TIMEOUT);
         *abort_flag = 1;
         return false;
@@ -137,8 +140,9 @@ __device__ __forceinline__ bool sh_wait(uint64_t* bar, uint32_t parity, int* sta
     }
   }
 }
-__device__ __forceinline__ bool sh_wait_warp(uint64_t* bar, uint32_t parity, int* status, volatile int* abort_flag) {
-  const bool ok = sh_wait(bar, parity, status, abort_flag);
+__device__ __forceinline__ bool sh_wait_warp(uint64_t* bar, uint32_t parity, int* status, volatile int* abort_flag,
+                                             uint64_t limit_ns = kWaitLimitNs) {
+  const bool ok = sh_wait(bar, parity, status, abort_flag, limit_ns);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -922,10 +926,37 @@ __device__ __forceinline__ void sh_issue_pv(uint32_t d_tmem, uint32_t p_tmem, ui
             (accumulate || kk > 0) ? 1u : 0u);
 }
 
+// After a wait that ran out: every (row, query head) of the run's pieces gets a
+// NaN record (the combine makes it NaN), or a NaN output where its piece would
+// have finished it.  By the 256 threads of the softmax warps.
+template <int D>
+__device__ __noinline__ void sh_poison(const SharedPlan& sp, int run) {
+  const int G = sp.p.d.G, Hq = sp.p.d.Hq;
+  PieceCursor cur = run_cursor(sp, run);
+  Piece pc;
+  while (cur.next(&pc)) {
+    for (int u = (int)threadIdx.x - 128; u < pc.b.n_rows * G; u += 256) {
+      const int j = u / G, head_l = u - j * G, r = pc.b.row0 + j, h = pc.g * G + head_l;
+      const int slot = j >= sp.rpt ? 1 : 0;   // (only a block of two tiles of rows has a second one)
+      const bool own = sp.p.d.row_tiles[r + 1] > sp.p.d.row_tiles[r];
+      if (pc.whole() && !own) {
+        const int64_t ob = (int64_t)r * sp.p.d.out.sr + (int64_t)h * sp.p.d.out.sh;
+        for (int d = 0; d < D; ++d) store_from_float(sp.p.d.out.out, ob + d, sp.p.d.out.type, qnan());
+      } else {
+        const int64_t rec = pc.i0 == 0 ? (int64_t)r * Hq + h
+                                       : (int64_t)sp.p.d.R * Hq + (int64_t)run * 256 + slot * 128 +
+                                             (j - slot * sp.rpt) * G + head_l;
+        sp.rec_ml[2 * rec] = qnan();
+        sp.rec_ml[2 * rec + 1] = qnan();
+      }
+    }
+  }
+}
+
 template <typename KT, int D, bool PLAIN>
 __global__ void __launch_bounds__(ShLayout<D>::THREADS, 1)
 shared_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-              const __grid_constant__ CUtensorMap tmV, const SharedPlan sp) {
+              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ SharedPlan sp) {
   using L = ShLayout<D>;
   constexpr int NK = L::NK, NV = L::NV;
   extern __shared__ unsigned char smem_raw[];
@@ -952,6 +983,7 @@ shared_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     mbar_init(B.merge_full, kShRows);
     mbar_init(B.merge_empty, kShRows);
     mbar_init(B.mma_done, 1);
+    mbar_init(B.never, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -980,7 +1012,9 @@ shared_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     // ---- softmax warpgroups ----
     setmaxnreg_inc<L::HIGH_REGS>();
     const int slot = (warp >> 2) - 1;
-    if (slot < L::NSLOT)
+    // (the test of the bounded waits: nothing arrives at this barrier)
+    const bool go = sp.stall_ns == 0 || sh_wait_warp(B.never, 0, status, abort_flag, sp.stall_ns);
+    if (go && slot < L::NSLOT)
       sh_softmax<KT, D, PLAIN>(sp, cur, sm, B, abort_flag, bad_flag, tmem, slot, warp & 3, lane, run);
   } else {
     setmaxnreg_dec<L::LOW_REGS>();
@@ -1150,6 +1184,7 @@ shared_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 
   tc_fence_before();
   __syncthreads();
+  if (warp >= 4 && *abort_flag) sh_poison<D>(sp, run);
   if (warp == 1) {
     tc_fence_after();
     mbar_wait_bounded(B.mma_done, 0, status);
