@@ -261,6 +261,7 @@ struct PagedPlan {
   int32_t n_tables, width;
   const int32_t* row_table;   // [R] or NULL (row r reads table r)
   const int32_t* own_lo;      // [R] or NULL: the first cell of row r's own part (shared prefixes)
+  uint64_t stall_ns;          // > 0: every warp first waits that long on a barrier nothing arrives at, and gives up
 };
 
 // Paged decode on the balanced persistent scheme of decode_stream.cu.

@@ -206,8 +206,6 @@ int32_t check_paged(const attn_paged_args* a, int32_t op_id) {
     return refuse(ATTN_ERR_UNSUPPORTED, "%s: zero q stride", op);
   if ((int64_t)a->n_rows * a->n_head_q > 0x7fffffffLL)
     return refuse(ATTN_ERR_UNSUPPORTED, "%s: too many rows", op);
-  if (a->reserved[0] != 0 && !runs_shared(a, op_id))
-    return refuse(ATTN_ERR_INVALID_ARG, "%s: the bounded-wait test runs on the tensor-core kernel only", op);
   return ATTN_OK;
 }
 
@@ -290,6 +288,7 @@ void fill_plan(PagedPlan* p, const attn_paged_args* a, const PagedWs& wl, char* 
   p->table = a->page_table; p->table_sr = a->table_stride;
   p->n_tables = a->n_tables; p->width = a->table_width;
   p->row_table = a->row_table;
+  p->stall_ns = (uint64_t)a->reserved[0] * 1000ull;
 }
 
 // The plan of the shared part (the softcap's series as in api.cu: the odd
@@ -298,6 +297,7 @@ void fill_shared(SharedPlan* sp, const PagedPlan& p, const attn_paged_args* a, c
   memset(sp, 0, sizeof(*sp));
   sp->p = p;
   sp->p.own_lo = nullptr;
+  sp->p.stall_ns = 0;
   sp->n_groups = a->n_groups;
   sp->group_begin = a->group_begin; sp->group_len = a->group_len;
   sp->n_slot = shared_slots(a->head_dim);
@@ -380,6 +380,7 @@ int32_t run_paged(const attn_paged_args* a, int32_t op, void* ws, size_t ws_byte
     if ((st = pool_map(&sV, a->v, a, sp.box_cells)) != ATTN_OK) return st;
     if ((e = launch_shared(sp, tmQ, sK, sV, s)) != cudaSuccess)
       return refuse(ATTN_ERR_CUDA, "shared decode launch: %s", cudaGetErrorString(e));
+    p.stall_ns = 0;             // (sp's own is the test's)
     p.own_lo = sp.own_lo;       // the stream kernel takes the rows' own cells, planned above
     p.d.plan_inline = 0;
     if ((e = launch_paged_stream(p, tmK, tmV, s)) != cudaSuccess)

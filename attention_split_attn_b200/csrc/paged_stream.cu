@@ -50,8 +50,8 @@ struct PsRing {
   static constexpr int NS = 2;                       // ring stages per warp
   static constexpr int TILE = kWarpTile * D * ES;    // K (or V) of one tile
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int BAR_OFF = NS * STAGE;
-  static constexpr int SLOT_OFF = BAR_OFF + NS * 8;  // first pool slot of the last 2 NS tiles issued
+  static constexpr int BAR_OFF = NS * STAGE;         // a barrier per stage, and one that nothing arrives at
+  static constexpr int SLOT_OFF = BAR_OFF + (NS + 1) * 8;   // first pool slot of the last 2 NS tiles issued
   static constexpr int RT_OFF = SLOT_OFF + 2 * NS * 4;   // inline row tile prefix [kInlineRows + 1]
   static constexpr int TOTAL = RT_OFF + (kInlineRows + 1) * 8 + 1024;   // + alignment slack for the swizzle
 };
@@ -128,7 +128,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   volatile int32_t* slots = reinterpret_cast<volatile int32_t*>(smem + Ring::SLOT_OFF);
   const int lane = threadIdx.x;
   if (lane == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i <= NS; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
   __syncwarp();
@@ -237,10 +237,12 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   st.init_offsets(lane);
   st.load_q(p.d, c.r, c.g * p.d.G, lane);
 
-  bool aborted = false;
+  bool aborted = p.stall_ns > 0;   // (the test of the bounded waits)
+  if (aborted) mbar_wait_bounded(&full[NS], 0, p.d.status, p.stall_ns);
+  __syncwarp();
   int64_t k = 0;
   if constexpr (Tr::ES == 1) st.prefetch_slot(p.d, c.g, slots[0], lane);
-  for (; k < n; ++k) {
+  for (; k < n && !aborted; ++k) {
     const int stg = (int)(k % NS);
     if constexpr (Tr::ES == 1) {
       st.take_prefetched();
@@ -249,7 +251,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         st.prefetch_slot(p.d, g, slots[(k + 1) % (2 * NS)], lane);
       }
     }
-    if (!mbar_wait_bounded(&full[stg], (uint32_t)((k / NS) & 1), p.d.status)) {
+    // (the lanes go on or give up together)
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[stg], (uint32_t)((k / NS) & 1), p.d.status))) {
       aborted = true;
       break;
     }
@@ -287,10 +290,16 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     }
   }
   if (aborted) {
-    // poison the record in progress and leave no copy in flight
-    const int64_t pair = (int64_t)c.r * Hkv + c.g;
-    const int64_t pair_start = Hkv * row_tiles[c.r] + (int64_t)c.g * c.nt;
-    st.write_partial(p.d.part.o, p.d.part.ml, pair_start >= t0 ? W + pair : w, p.d.G, lane, true);
+    // poison the record in progress and those of the run's later pairs (the
+    // workspace may hold an earlier call's), and leave no copy in flight
+    for (;;) {
+      const int64_t pair = (int64_t)c.r * Hkv + c.g;
+      const int64_t pair_start = Hkv * row_tiles[c.r] + (int64_t)c.g * c.nt;
+      st.write_partial(p.d.part.o, p.d.part.ml, pair_start >= t0 ? W + pair : w, p.d.G, lane, true);
+      if (pair_start + c.nt >= t1) break;
+      c.j = c.nt - 1;
+      ps_next(p, row_tiles, c);
+    }
     if (lane == 0)
       for (int64_t kk = k; kk < issued; ++kk) mbar_wait_bounded(&full[kk % NS], (uint32_t)((kk / NS) & 1), nullptr);
     __syncwarp();

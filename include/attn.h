@@ -437,7 +437,8 @@ typedef struct {
     const float *alibi_slopes, *sinks;       /* [n_head_q] or NULL              */
     const float *k_scale, *v_scale; int64_t scale_stride_cell;   /* e4m3 / int8: by slot */
     int32_t reserved[4];   /* must be zero, except reserved[0]: a test of the bounded waits as in attn_prefill
-                              (attn_args), for the kernel that reads shared cells; its rows become NaN */
+                              (attn_args), of the kernel that reads shared cells where one runs, else of the
+                              one that reads single rows'; the rows that it reads cells of become NaN */
 } attn_paged_args;
 
 /* As attn_supports / attn_workspace_size, for ATTN_OP_DECODE_PAGED and

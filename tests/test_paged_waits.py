@@ -61,3 +61,20 @@ def test_shared_rows_of_a_timed_out_run_are_nan(cuda_lib, rows, Hq, end, D):
     assert torch.isnan(bad[:rows]).all()
     assert torch.equal(bad[rows:], good[rows:])
     assert torch.equal(again, good)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("op", [A.OP_DECODE_PAGED, A.OP_DECODE_SHARED])
+@pytest.mark.parametrize("rows,longest,over", [(1500, 40, dict(D=64, Hq=4, Hkv=4)), (7, 3000, {}),
+                                               (700, 50, dict(cache="e4m3", Hq=8, Hkv=8)),
+                                               (600, 60, dict(D=256, Hq=32, Hkv=2))])
+def test_single_rows_of_a_timed_out_warp_are_nan(cuda_lib, rows, longest, over, op):
+    """More (row, KV head) pairs than warps, so that a warp's run holds several, and rows over many warps."""
+    ends = [(7 * i) % longest for i in range(rows)]
+    c = Case(62, ends, P=16, **over)
+    want = c.expected()
+    good, bad, again = _stalled(c, op)
+    compare(good, want, 1e-5, 2e-2)
+    sees = torch.tensor(ends) > 0
+    assert torch.isnan(bad[sees.cuda()]).all() and (bad[~sees.cuda()] == 0).all()
+    assert torch.equal(again, good)
