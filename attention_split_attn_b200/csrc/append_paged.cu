@@ -99,11 +99,14 @@ __global__ void __launch_bounds__(kApThreads) append_copy_kernel(const attn_appe
   }
 }
 
-// x / s toward zero with the last bit set when it is not exact.  With inv =
-// 1 / s and s far from the ends of the range: one Newton step puts q within an
-// ulp of the quotient, where the remainder x - q s is exact; a remainder of the
-// other sign means that q lies beyond the quotient, and one step of its bits
-// back truncates it.  (A division per value took 79% of the issue slots.)
+// x / s rounded to odd (toward zero, the last bit set when that is not exact:
+// S. Boldo and G. Melquiond, "Emulation of a FMA and correctly rounded sums",
+// 2008).  div_odd_fast, for s far from the ends of the range and inv = 1 / s:
+// one Newton step on the quotient (P. Markstein's division with a fused
+// multiply-add, 1990) puts q within an ulp of it, where the remainder x - q s
+// is exact; a remainder of the other sign means that q lies beyond the
+// quotient, and one step of its bits back truncates it.  (A division per value
+// took 79% of the issue slots.)
 __device__ __forceinline__ float div_odd_fast(float x, float s, float inv) {
   const float q0 = x * inv;
   const float q = fmaf(fmaf(-q0, s, x), inv, q0);
@@ -112,7 +115,12 @@ __device__ __forceinline__ float div_odd_fast(float x, float s, float inv) {
   if (rem == 0.f) return q;
   return __uint_as_float((b - ((b ^ __float_as_uint(rem)) >> 31)) | 1u);
 }
+// At the ends: x and s of 1e-30 and below are scaled up, or the remainder would
+// be a fraction of the smallest float and round to 0 (a tie that is none).
 __device__ __forceinline__ float div_odd(float x, float s) {
+  const float up = s < 1.f ? 0x1p96f : 1.f;
+  x *= up;
+  s *= up;
   const float q = __fdiv_rz(x, s);
   const float rem = fmaf(-q, s, x);
   return rem != 0.f ? __uint_as_float(__float_as_uint(q) | 1u) : q;
