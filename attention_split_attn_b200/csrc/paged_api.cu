@@ -129,7 +129,7 @@ int32_t check_append(const attn_append_args* a) {
   if (!aligned16(a->k_new) || !aligned16(a->v_new) || (a->n_rows > 1 && (a->new_stride_row * es) % 16) ||
       (a->n_head_kv > 1 && (a->new_stride_head * es) % 16))
     return refuse(ATTN_ERR_UNSUPPORTED, "%s: new rows and their strides must be multiples of 16 bytes", op);
-  if ((int64_t)a->n_rows * a->n_head_kv > (1LL << 33))
+  if (a->n_rows > (1 << 30) || (int64_t)a->n_rows * a->n_head_kv > (1LL << 33))   // (the kernels' row numbers are int32)
     return refuse(ATTN_ERR_UNSUPPORTED, "%s: too many rows", op);
   return ATTN_OK;
 }

@@ -383,7 +383,7 @@ int32_t attn_page_tables(const attn_page_args *args, void *stream);
  * The scales go to k_scale / v_scale[slot * scale_stride_cell + head].
  * New rows, cache and strides are multiples of 16 bytes.                   */
 typedef struct {
-    int32_t n_rows, n_head_kv, head_dim;     /* head_dim 64, 128 or 256         */
+    int32_t n_rows, n_head_kv, head_dim;     /* head_dim 64, 128 or 256; n_rows up to 2^30 */
     int32_t n_pages, page_size;              /* n_pages * page_size < 2^31      */
     const void *k_new, *v_new; int32_t new_type;
     int64_t new_stride_row, new_stride_head; /* elements                        */
