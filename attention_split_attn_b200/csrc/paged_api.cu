@@ -72,6 +72,15 @@ int32_t check_scales(const char* op, int32_t type, int32_t n_pages, int32_t page
   return ATTN_OK;
 }
 
+// Whether two arrays of int32 share an entry.
+struct I32Array {
+  const int32_t* p;
+  int64_t n;
+};
+bool overlap(const I32Array& x, const I32Array& y) {
+  return x.p && y.p && x.n > 0 && y.n > 0 && x.p < y.p + y.n && y.p < x.p + x.n;
+}
+
 int32_t check_pages(const attn_page_args* a) {
   const char* op = "page_tables";
   if (!a) return refuse(ATTN_ERR_INVALID_ARG, "args is NULL");
@@ -99,6 +108,17 @@ int32_t check_pages(const attn_page_args* a) {
     if (a->seq_len == a->seq_len_out)
       return refuse(ATTN_ERR_INVALID_ARG, "%s: seq_len_out must not be the input array", op);
   }
+  // every CTA reads the inputs while others write: an array that is written is no other one's
+  const int64_t n = a->n_seqs, rows = a->n_rows;
+  const I32Array all[] = {
+      {a->slot, rows}, {a->row_seq, rows}, {a->row_end, rows}, {a->seq_row, n + 1}, {a->seq_len_out, n},
+      {a->free_state_out, 2}, {a->page_table, n > 0 ? (n - 1) * a->table_stride + a->table_width : 0},
+      {a->free_ring, a->n_pages}, {a->seq_len, n}, {a->new_len, n}, {a->n_keep, n}, {a->free_state, 2}};
+  constexpr int kWritten = 8, kAll = sizeof(all) / sizeof(all[0]);
+  for (int i = 0; i < kWritten; ++i)
+    for (int j = i + 1; j < kAll; ++j)
+      if (overlap(all[i], all[j]))
+        return refuse(ATTN_ERR_INVALID_ARG, "%s: an array that is written overlaps another one", op);
   return ATTN_OK;
 }
 

@@ -340,14 +340,20 @@ enum { ATTN_OP_DECODE_PAGED = 4, ATTN_OP_DECODE_SHARED = 5 };
  * The step's rows are numbered sequence after sequence (seq_row: where each
  * sequence's rows begin, counted on past n_rows where they do not fit); row t
  * gets its slot, its sequence and the number of cells it may see, position + 1.
- * A sequence that cannot grow -- the ring is empty, the table row is full, its
- * rows pass n_rows -- is left as it was: its length and table do not change,
- * its rows get slot -1 and row_end 0, and seq_len_out shows it.  Rows behind
- * the last sequence get slot -1, row_seq -1 and row_end 0.
+ * A sequence that cannot grow -- the ring has no pages left, the table row is
+ * full, its rows pass n_rows -- is left as it was: its length and table do not
+ * change, its rows get slot -1 and row_end 0, and seq_len_out shows it.  The
+ * ring is asked in sequence order and by the step's start: a sequence that
+ * needs pages gets them if it and all sequences before it that have room in
+ * their table rows together need no more than were free then (so one that asks
+ * for too many stops those behind it that need a page, and the pages that a
+ * step returns are there for the next).  Rows behind the last sequence get slot
+ * -1, row_seq -1 and row_end 0.
  * Table entries and page ids are checked: a length outside [0, table_width *
  * page_size], an id outside [0, n_pages), a ring state that cannot be, or more
  * pages returned than the ring holds record ATTN_ERR_INVALID_ARG in the
- * device status word, and the cells concerned get slot -1.               */
+ * device status word, and the cells concerned get slot -1.  The arrays that are
+ * written overlap no other one.                                            */
 typedef struct {
     int32_t n_seqs;             /* 0 .. 16384                                   */
     int32_t page_size;          /* cells per page, >= 1                         */
@@ -408,7 +414,9 @@ int32_t attn_append_paged(const attn_append_args *args, void *stream);
  * Types: a 16-bit cache with Q in its dtype, head_dim 64, 128 or 256, up to 16
  * query heads per KV head; or an e4m3 / int8 cache (scales indexed by slot)
  * with Q in F16 or BF16, head_dim 128 or 256, up to 8.  Any of F32, F16, BF16
- * out.  page_size is a multiple of 16; Q is 16-byte aligned with strides that
+ * out.  Sums, maxima and statistics are held in F32; a weight is rounded once,
+ * to the cache's type (for e4m3 / int8: to F16, its cell's V scale folded in),
+ * before it meets V.  page_size is a multiple of 16; Q is 16-byte aligned with strides that
  * are multiples of 16 bytes, and so is the cache.
  * attn_decode_shared: rows group_begin[i] .. group_begin[i + 1] - 1 form group
  * i, and the first group_len[i] cells of their tables are the same; they are
