@@ -17,8 +17,8 @@
 // on), and the table entries that are read (below held) and written (from
 // held on), are disjoint, and the counters have separate in and out arrays.
 // The work is bound by launch latency and two dependent loads (length, then
-// table or ring entry): about 12 bytes written per row.  3.6 us a call for 16
-// sequences (the launch and the host call), 8.3 us for 509 sequences and about
+// table or ring entry): about 12 bytes written per row.  3.8 us a call for 16
+// sequences (the launch and the host call), 8.4 us for 509 sequences and about
 // 50000 rows.
 #include <algorithm>
 

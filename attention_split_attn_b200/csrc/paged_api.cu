@@ -154,10 +154,11 @@ int32_t check_append(const attn_append_args* a) {
   return ATTN_OK;
 }
 
-// Sharing takes four launches and a plan, about 10 us more than row by row,
+// Sharing takes four launches and a plan, 10 to 20 us more than row by row,
 // and saves at most the reading of all rows' tables.  Below 64 MB of them (at
 // 5.4 TB/s 12 us) row by row is the faster form whatever the groups: 8 rows
-// of 1100 cells, 8 KV heads, D 128 (38 MB) take 16 us against 25 us.
+// of 1100 cells, 8 KV heads, D 128 (38 MB) take 13 us against 32 us.  The rule
+// sees what the tables can hold, not the lengths, which are on the device.
 constexpr int64_t kShareBytes = 64LL << 20;
 bool runs_shared(const attn_paged_args* a, int32_t op) {
   if (op != ATTN_OP_DECODE_SHARED || !is16(a->kv_type) || a->n_groups == 0 || a->n_pages == 0) return false;

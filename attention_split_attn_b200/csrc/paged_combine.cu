@@ -6,7 +6,7 @@
 //
 // Bound by the latency of a few dependent loads (the row's place, its records'
 // places, the records) and, for one long row, by the number of its records:
-// 1924 warps leave 240 of them per (row, KV head) at 8 KV heads, which one warp
+// 1776 warps leave 222 of them per (row, KV head) at 8 KV heads, which one warp
 // took 35 us to fold.  So
 //  * `wpi` warps of a CTA share an item (row, query head) while the items alone
 //    would leave the SMs short of warps: warp w takes the records w, w + wpi,
@@ -169,7 +169,8 @@ template <bool SHARED>
 cudaError_t launch_t(const SharedPlan& sp, const PagedPlan& own, int sms, cudaStream_t stream) {
   // Warps per item 8, 4, 2 while items x warps stay within the 24 resident warps per SM,
   // then items per warp 1 .. 32 to stay there (131072 items of a prompt: 58 us
-  // at 32 items a warp, 77 at 8, where the lookups of four times the warps cost more).
+  // at 32 items a warp, 77 at 8, where the lookups of four times the warps cost more;
+  // 52 us since the sinks are read with the lookups).
   const int64_t items = (int64_t)own.d.R * own.d.Hq, room = 24LL * sms;
   int wpi = kCombWarps;
   while (wpi > 1 && items * wpi > room) wpi >>= 1;
