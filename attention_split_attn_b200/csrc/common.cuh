@@ -178,15 +178,14 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 }
 
 // Wait for the phase with the given parity to complete, for at most about
-// limit_ns.  Returns false (and records a timeout) if it never does.
+// kWaitLimitNs.  Returns false (and records a timeout) if it never does.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s
-__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, int* status,
-                                                  uint64_t limit_ns = kWaitLimitNs) {
+__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, int* status) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t spin = 1;; ++spin) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((spin & 63u) == 0 && global_timer_ns() - t0 > limit_ns) {
+    if ((spin & 63u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) {
       record_status(status, ATTN_ERR_DEVICE_TIMEOUT);
       return false;
     }

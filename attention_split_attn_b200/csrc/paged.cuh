@@ -54,6 +54,15 @@ __device__ __forceinline__ int run_of(int64_t t, int64_t T, int64_t W) {
   return (int)div64((t + 1) * W + T - 1, T) - 1;
 }
 
+// The test of the bounded waits: `bar`, which nothing arrives at, for limit_ns;
+// records the timeout as mbar_wait_bounded does.
+__device__ __forceinline__ void stall_bounded(uint64_t* bar, uint64_t limit_ns, int* status) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, 0) && global_timer_ns() - t0 <= limit_ns) {
+  }
+  record_status(status, ATTN_ERR_DEVICE_TIMEOUT);
+}
+
 // 4-D tiled TMA load into shared memory, completing on `bar` (tx bytes).
 __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
                                             int c2, int c3, uint64_t cache_hint) {

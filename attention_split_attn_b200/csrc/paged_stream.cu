@@ -238,7 +238,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   st.load_q(p.d, c.r, c.g * p.d.G, lane);
 
   bool aborted = p.stall_ns > 0;   // (the test of the bounded waits)
-  if (aborted) mbar_wait_bounded(&full[NS], 0, p.d.status, p.stall_ns);
+  if (aborted) stall_bounded(&full[NS], p.stall_ns, p.d.status);
   __syncwarp();
   int64_t k = 0;
   if constexpr (Tr::ES == 1) st.prefetch_slot(p.d, c.g, slots[0], lane);
